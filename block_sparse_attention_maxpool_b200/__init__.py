@@ -28,7 +28,10 @@ __all__ = ["MsaError", "Shape", "msa_indexer_append", "msa_kv_append", "msa_step
            "msa_sparse_attn_prefill_paged", "DsaShape", "DSA_SEL_WIDTH", "msa_dsa_indexer_append",
            "msa_dsa_token_scores", "msa_dsa_select_topk", "msa_dsa_sparse_attn_decode", "dsa_decode_step",
            "msa_decode_step_fused", "msa_decode_step_fused_workspace_bytes", "decode_step_fused", "DecodeGraph",
-           "StepPipeline", "msa_wait_selftest", "WAIT_SELFTEST_WORKSPACE_BYTES"]
+           "StepPipeline", "msa_wait_selftest", "WAIT_SELFTEST_WORKSPACE_BYTES",
+           "Rope", "msa_rope_append", "msa_kv_append_fp8", "msa_kv_append_fp8_workspace_bytes",
+           "msa_sparse_attn_decode_fp8", "msa_sparse_attn_prefill_fp8", "msa_window_attn_decode",
+           "msa_window_attn_prefill", "msa_attn_workspace_bytes", "window_step", "fp8_caches"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmsa.so")
 MODE_DECODE = 0
@@ -114,6 +117,24 @@ class DsaShape:
                          int(bool(self.relu)))
 
 
+class CRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+@dataclass(frozen=True)
+class Rope:
+    """Position rotation (msa_rope): ``inv_freq`` is a float64 device tensor
+    [rot_dim / 2], the angle of pair i at position p is p * inv_freq[i]."""
+    inv_freq: torch.Tensor
+    interleaved: bool = False
+
+    def c(self, dev) -> CRope:
+        f = self.inv_freq
+        if f.dim() != 1:
+            raise ValueError("inv_freq must be 1-D")
+        return CRope(_dptr(f, torch.float64, f.shape, "inv_freq", dev), 2 * f.shape[0], int(bool(self.interleaved)))
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -166,6 +187,25 @@ _SIGS.update({
                                              _P, _P, _I, ctypes.c_float, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "msa_decode_step_fused_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(CShape), _I]),
     "msa_wait_selftest": (ctypes.c_int, [ctypes.c_longlong, _P, ctypes.c_size_t, _P]),
+})
+_RP = ctypes.POINTER(CRope)
+_SH = ctypes.POINTER(CShape)
+_F = ctypes.c_float
+_Z = ctypes.c_size_t
+_SIGS.update({
+    "msa_rope_append": (ctypes.c_int, [_SH, _PG, _RP, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I,
+                                       _P]),
+    "msa_kv_append_fp8": (ctypes.c_int, [_SH, _PG, _RP, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _Z, _P]),
+    "msa_kv_append_fp8_workspace_bytes": (_Z, [_SH, _I]),
+    "msa_sparse_attn_decode_fp8": (ctypes.c_int, [_SH, _PG, _P, _P, _P, _P, _P, _P, _P, _P, _I, _F, _P, _P, _Z, _P]),
+    "msa_sparse_attn_prefill_fp8": (ctypes.c_int, [_SH, _PG, _P, _P, _P, _P, _P, _P, _P, _P, _I, _F, _P, _P, _Z, _P]),
+    "msa_window_attn_decode": (ctypes.c_int, [_SH, _PG, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _Z, _P]),
+    "msa_window_attn_prefill": (ctypes.c_int, [_SH, _PG, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _Z, _P]),
+    "msa_window_attn_decode_fp8": (ctypes.c_int, [_SH, _PG, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _Z,
+                                                  _P]),
+    "msa_window_attn_prefill_fp8": (ctypes.c_int, [_SH, _PG, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _Z,
+                                                   _P]),
+    "msa_attn_workspace_bytes": (_Z, [_SH, _I, _I]),
 })
 
 
@@ -495,7 +535,7 @@ def msa_version() -> int:
 
 
 def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None, stream=None,
-                prefill: bool = False, pages: Pages | None = None):
+                prefill: bool = False, pages: Pages | None = None, rope: Rope | None = None):
     """One MSA step through the C ABI: append the new tokens' indexer keys
     and K/V rows, score blocks, select the top-k and attend.
 
@@ -504,10 +544,18 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
     idx_k_new, k_new, v_new, q_stream, q_pos, idx_q, q (device).  ``bufs`` may
     hold preallocated block_scores / sel / n_sel / out / workspace.  With
     ``pages`` the caches are page pools addressed through its block table.
+    With ``rope`` the new keys and the queries (idx_k_new, k_new, idx_q, q)
+    arrive unrotated and are rotated on the way (bufs: q_rot, idx_q_rot).
+    k_cache and v_cache may be 8-bit (float8_e4m3fn, with k_scale and v_scale
+    in ``caches``; bufs: workspace_fp8).
     Returns (out, sel, n_sel, block_scores).
     """
     b = bufs or {}
-    if caches["idx_k_cache"].dtype == torch.float16:
+    fp8 = caches["k_cache"].dtype is torch.float8_e4m3fn
+    if rope is not None or fp8:
+        q, idx_q = _append_step(shape, caches, new, b, stream, pages, rope, True)
+        new = dict(new, q=q, idx_q=idx_q)
+    elif caches["idx_k_cache"].dtype == torch.float16:
         msa_indexer_append_f16(shape, caches["idx_k_cache"], new["idx_k_new"], new["tok_stream"], new["tok_pos"],
                                stream, pages)
         msa_kv_append(shape, caches["k_cache"], caches["v_cache"], new["k_new"], new["v_new"],
@@ -522,6 +570,12 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
                                           device=new["q"].device))
     bs = msa_block_scores(shape, new["idx_q"], caches["idx_k_cache"], new["q_stream"], new["q_pos"],
                           b.get("block_scores"), stream, b.get("workspace"), pages)
+    if fp8:
+        sel, n_sel = msa_select_topk(shape, bs, new["q_pos"], b.get("sel"), b.get("n_sel"), stream)
+        attend = msa_sparse_attn_prefill_fp8 if prefill else msa_sparse_attn_decode_fp8
+        out = attend(shape, new["q"], caches["k_cache"], caches["v_cache"], caches["k_scale"], caches["v_scale"], sel,
+                     new["q_stream"], new["q_pos"], None, b.get("out"), None, stream, pages)
+        return out, sel, n_sel, bs
     if not prefill:                         # the top-16 inside the attention kernel
         out, sel, n_sel = msa_select_attn_decode(shape, bs, new["q"], caches["k_cache"], caches["v_cache"],
                                                  new["q_stream"], new["q_pos"], None, b.get("sel"), b.get("n_sel"),
@@ -531,6 +585,275 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
     out = msa_sparse_attn_prefill(shape, new["q"], caches["k_cache"], caches["v_cache"], sel, new["q_stream"],
                                   new["q_pos"], None, b.get("out"), b.get("workspace"), stream, pages)
     return out, sel, n_sel, bs
+
+
+# ---- rotating appends, 8-bit caches, window attention ---------------------------
+def _dptr(t: torch.Tensor, dtype, shape, name: str, dev) -> int:
+    """_ptr of a tensor that has to be on ``dev``, the call's device."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, dtype, shape, name)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return p
+
+
+def _device_of(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _on(dev, stream):
+    """The raw stream a call on ``dev`` launches on."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _stream(stream)
+
+
+def _launch(fn: str, dev, args) -> None:
+    """Call ``fn`` with ``dev`` as the current device (the library launches on it)."""
+    f = getattr(library(), fn)
+    if dev.index == torch.cuda.current_device():
+        status = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args)
+    _check(fn, status)
+
+
+def _pages_arg(shape: Shape, pages: Pages | None, dev):
+    """The msa_pages argument (None: contiguous caches)."""
+    if pages is None:
+        return None
+    return CPages(_dptr(pages.block_table, torch.int32, (shape.n_streams, shape.n_blocks), "block_table", dev),
+                  pages.n_pages)
+
+
+def _scale_shape(shape: Shape, pages: Pages | None) -> tuple:
+    if pages is None:
+        return (shape.n_streams, shape.n_kv_heads, shape.n_blocks)
+    return (pages.n_pages, shape.n_kv_heads)
+
+
+def fp8_caches(shape: Shape, device, n_pages: int | None = None) -> dict:
+    """Empty 8-bit caches of ``shape`` (with ``n_pages``: page pools):
+    k_cache, v_cache (float8_e4m3fn) and their scales k_scale, v_scale."""
+    rows, sc = (shape.n_streams, shape.n_kv_heads, shape.capacity), (shape.n_streams, shape.n_kv_heads, shape.n_blocks)
+    if n_pages is not None:
+        rows, sc = (n_pages, shape.n_kv_heads, shape.block), (n_pages, shape.n_kv_heads)
+    out = {}
+    for name in ("k", "v"):
+        out[name + "_cache"] = torch.zeros(rows + (shape.head_dim,), dtype=torch.uint8,
+                                           device=device).view(torch.float8_e4m3fn)
+        out[name + "_scale"] = torch.zeros(sc, dtype=torch.float32, device=device)
+    return out
+
+
+def msa_rope_append(shape: Shape, rope: Rope, k_cache=None, v_cache=None, k_new=None, v_new=None, tok_stream=None,
+                    tok_pos=None, q=None, q_pos=None, q_out=None, idx_k_cache=None, idx_k_new=None, idx_q=None,
+                    idx_q_out=None, stream=None, pages: Pages | None = None):
+    """A step's appends with the position rotation applied on the way, and its
+    queries rotated, in one launch.  K/V rows (k_cache .. v_new), indexer
+    keys (idx_k_cache: float32 or float16) and the queries q, idx_q are each
+    optional.  Returns (q_out, idx_q_out), allocated here when None; pass an
+    input as its output to rotate it in place."""
+    lead = next((t for t in (tok_pos, q_pos) if t is not None), None)
+    if lead is None:
+        raise ValueError("tok_pos or q_pos is required")
+    dev = _device_of(lead, "tok_pos" if tok_pos is not None else "q_pos")
+    G, D, Di = shape.n_kv_heads, shape.head_dim, shape.idx_dim
+    nt = 0 if tok_pos is None else _n(tok_pos, "tok_pos")
+    nq = 0 if q_pos is None else _n(q_pos, "q_pos")
+    if (q is not None or idx_q is not None) and q_pos is None:
+        raise ValueError("q and idx_q need q_pos")
+    given = [t is not None for t in (k_cache, v_cache, k_new, v_new)]
+    if any(given) != all(given) or (idx_k_cache is None) != (idx_k_new is None):
+        raise ValueError("a cache and its new rows come together")
+    if (any(given) or idx_k_cache is not None) and (tok_stream is None or tok_pos is None):
+        raise ValueError("appended rows need tok_stream and tok_pos")
+    if q is None and idx_q is None:
+        nq = 0
+    if not any(given) and idx_k_cache is None:
+        nt = 0
+    if q is not None and q_out is None:
+        q_out = torch.empty((nq, shape.n_q_heads, D), dtype=torch.bfloat16, device=dev)
+    if idx_q is not None and idx_q_out is None:
+        idx_q_out = torch.empty((nq, G, Di), dtype=torch.float32, device=dev)
+    k = [0, 0, 0, 0, 0]
+    if any(given):
+        cs, ns = _cache_shape(shape, pages, D), (nt, G, D)
+        k = [_dptr(k_cache, torch.bfloat16, cs, "k_cache", dev), _dptr(v_cache, torch.bfloat16, cs, "v_cache", dev),
+             _dptr(k_new, torch.bfloat16, ns, "k_new", dev), _dptr(v_new, torch.bfloat16, ns, "v_new", dev)]
+    ik = [0, 0, 0]
+    if idx_k_cache is not None:
+        kdt = torch.float16 if idx_k_cache.dtype == torch.float16 else torch.float32
+        ik = [_dptr(idx_k_cache, kdt, _cache_shape(shape, pages, Di), "idx_k_cache", dev), int(kdt == torch.float16),
+              _dptr(idx_k_new, torch.float32, (nt, G, Di), "idx_k_new", dev)]
+    tk = [0, 0] if nt == 0 else [_dptr(tok_stream, torch.int32, (nt,), "tok_stream", dev),
+                                 _dptr(tok_pos, torch.int32, (nt,), "tok_pos", dev)]
+    qs, iqs = (nq, shape.n_q_heads, D), (nq, G, Di)
+    qp = [0, 0] if q is None else [_dptr(q, torch.bfloat16, qs, "q", dev), _dptr(q_out, torch.bfloat16, qs, "q_out", dev)]
+    ip = [0, 0] if idx_q is None else [_dptr(idx_q, torch.float32, iqs, "idx_q", dev),
+                                       _dptr(idx_q_out, torch.float32, iqs, "idx_q_out", dev)]
+    pp = 0 if nq == 0 else _dptr(q_pos, torch.int32, (nq,), "q_pos", dev)
+    _launch("msa_rope_append", dev, (shape.c(), _pages_arg(shape, pages, dev), rope.c(dev), *k[:4], *ik, *tk, nt, *qp,
+                                     *ip, pp, nq, _on(dev, stream)))
+    return q_out, idx_q_out
+
+
+def msa_kv_append_fp8_workspace_bytes(shape: Shape, n_tok: int) -> int:
+    v = library().msa_kv_append_fp8_workspace_bytes(shape.c(), n_tok)
+    if v == ctypes.c_size_t(-1).value:
+        raise MsaError("msa_kv_append_fp8_workspace_bytes", -3)
+    return v
+
+
+def msa_kv_append_fp8(shape: Shape, k_cache, v_cache, k_scale, v_scale, k_new, v_new, tok_stream, tok_pos,
+                      rope: Rope | None = None, workspace=None, stream=None, pages: Pages | None = None) -> None:
+    """Write new K rows (rotated when ``rope`` is given) and V rows into 8-bit
+    caches (float8_e4m3fn) with one scale per (128-token block, group);
+    a block whose scale grows has its older rows requantised."""
+    n = _n(tok_pos, "tok_pos")
+    dev = _device_of(tok_pos, "tok_pos")
+    cs, ss = _cache_shape(shape, pages, shape.head_dim), _scale_shape(shape, pages)
+    ns = (n, shape.n_kv_heads, shape.head_dim)
+    if workspace is None:
+        workspace = torch.empty((msa_kv_append_fp8_workspace_bytes(shape, n),), dtype=torch.uint8, device=dev)
+    _launch("msa_kv_append_fp8", dev, (
+        shape.c(), _pages_arg(shape, pages, dev), None if rope is None else rope.c(dev),
+        _dptr(k_cache, torch.float8_e4m3fn, cs, "k_cache", dev), _dptr(v_cache, torch.float8_e4m3fn, cs, "v_cache", dev),
+        _dptr(k_scale, torch.float32, ss, "k_scale", dev), _dptr(v_scale, torch.float32, ss, "v_scale", dev),
+        _dptr(k_new, torch.bfloat16, ns, "k_new", dev), _dptr(v_new, torch.bfloat16, ns, "v_new", dev),
+        _dptr(tok_stream, torch.int32, (n,), "tok_stream", dev), _dptr(tok_pos, torch.int32, (n,), "tok_pos", dev), n,
+        _dptr(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel(), _on(dev, stream)))
+
+
+def msa_attn_workspace_bytes(shape: Shape, n_q: int, mode: int) -> int:
+    """Workspace of the window and 8-bit attention calls."""
+    v = library().msa_attn_workspace_bytes(shape.c(), n_q, mode)
+    if v == ctypes.c_size_t(-1).value:
+        raise MsaError("msa_attn_workspace_bytes", -3)
+    return v
+
+
+def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_scale, extra, q_stream, q_pos, tail,
+              softmax_scale, out, workspace, stream, pages):
+    n = _n(q_pos, "q_pos")
+    dev = _device_of(q, "q")
+    qs = (n, shape.n_q_heads, shape.head_dim)
+    if out is None:
+        out = torch.empty(qs, dtype=torch.bfloat16, device=dev)
+    cs = _cache_shape(shape, pages, shape.head_dim)
+    if k_cache.dtype is torch.float8_e4m3fn:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an 8-bit cache needs k_scale and v_scale")
+        ss = _scale_shape(shape, pages)
+        kv = (_dptr(k_cache, torch.float8_e4m3fn, cs, "k_cache", dev),
+              _dptr(v_cache, torch.float8_e4m3fn, cs, "v_cache", dev),
+              _dptr(k_scale, torch.float32, ss, "k_scale", dev), _dptr(v_scale, torch.float32, ss, "v_scale", dev))
+        fn += "_fp8"
+    else:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to an 8-bit cache")
+        kv = (_dptr(k_cache, torch.bfloat16, cs, "k_cache", dev), _dptr(v_cache, torch.bfloat16, cs, "v_cache", dev))
+    wp = wb = 0
+    if workspace is None and mode == MODE_PREFILL:
+        need = msa_attn_workspace_bytes(shape, n, mode)
+        if need > 0:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        wp, wb = _dptr(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel()
+    if softmax_scale is None:
+        softmax_scale = shape.head_dim ** -0.5
+    _launch(fn, dev, (shape.c(), _pages_arg(shape, pages, dev), _dptr(q, torch.bfloat16, qs, "q", dev), *kv, *extra,
+                      _dptr(q_stream, torch.int32, (n,), "q_stream", dev), _dptr(q_pos, torch.int32, (n,), "q_pos", dev),
+                      n, *tail, softmax_scale, _dptr(out, torch.bfloat16, qs, "out", dev), wp, wb, _on(dev, stream)))
+    return out
+
+
+def _sparse_fp8(fn, mode, shape, q, k_cache, v_cache, k_scale, v_scale, sel, q_stream, q_pos, softmax_scale, out,
+                workspace, stream, pages):
+    if k_cache.dtype is not torch.float8_e4m3fn:
+        raise ValueError(f"k_cache must be {torch.float8_e4m3fn}, got {k_cache.dtype}")
+    s = _dptr(sel, torch.int32, (_n(q_pos, "q_pos"), shape.n_kv_heads, shape.top_k), "sel", _device_of(q, "q"))
+    return _ext_attn(fn, mode, shape, q, k_cache, v_cache, k_scale, v_scale, (s,), q_stream, q_pos, (), softmax_scale,
+                     out, workspace, stream, pages)
+
+
+def msa_sparse_attn_decode_fp8(shape: Shape, q, k_cache, v_cache, k_scale, v_scale, sel, q_stream, q_pos,
+                               softmax_scale=None, out=None, workspace=None, stream=None,
+                               pages: Pages | None = None):
+    """msa_sparse_attn_decode over an 8-bit cache."""
+    return _sparse_fp8("msa_sparse_attn_decode", MODE_DECODE, shape, q, k_cache, v_cache, k_scale, v_scale, sel,
+                       q_stream, q_pos, softmax_scale, out, workspace, stream, pages)
+
+
+def msa_sparse_attn_prefill_fp8(shape: Shape, q, k_cache, v_cache, k_scale, v_scale, sel, q_stream, q_pos,
+                                softmax_scale=None, out=None, workspace=None, stream=None,
+                                pages: Pages | None = None):
+    """msa_sparse_attn_prefill over an 8-bit cache."""
+    return _sparse_fp8("msa_sparse_attn_prefill", MODE_PREFILL, shape, q, k_cache, v_cache, k_scale, v_scale, sel,
+                       q_stream, q_pos, softmax_scale, out, workspace, stream, pages)
+
+
+def msa_window_attn_decode(shape: Shape, q, k_cache, v_cache, q_stream, q_pos, window: int, n_sink: int = 0,
+                           softmax_scale=None, out=None, workspace=None, stream=None, pages: Pages | None = None,
+                           k_scale=None, v_scale=None):
+    """Attention over the last ``window`` slots of each query and the first
+    ``n_sink`` ones, for a few queries (decode).  The caches are bfloat16, or
+    float8_e4m3fn with their k_scale and v_scale."""
+    return _ext_attn("msa_window_attn_decode", MODE_DECODE, shape, q, k_cache, v_cache, k_scale, v_scale, (), q_stream,
+                     q_pos, (window, n_sink), softmax_scale, out, workspace, stream, pages)
+
+
+def msa_window_attn_prefill(shape: Shape, q, k_cache, v_cache, q_stream, q_pos, window: int, n_sink: int = 0,
+                            softmax_scale=None, out=None, workspace=None, stream=None, pages: Pages | None = None,
+                            k_scale=None, v_scale=None):
+    """msa_window_attn_decode for batches of many queries (prefill)."""
+    return _ext_attn("msa_window_attn_prefill", MODE_PREFILL, shape, q, k_cache, v_cache, k_scale, v_scale, (),
+                     q_stream, q_pos, (window, n_sink), softmax_scale, out, workspace, stream, pages)
+
+
+def _append_step(shape: Shape, caches: dict, new: dict, b: dict, stream, pages, rope, indexer: bool):
+    """A step's appends into bf16 or 8-bit caches, with or without rotation.
+    Returns the step's queries (q, idx_q), rotated when ``rope`` is given."""
+    fp8 = caches["k_cache"].dtype is torch.float8_e4m3fn
+    tok = (new["tok_stream"], new["tok_pos"])
+    q, idx_q = new["q"], new.get("idx_q") if indexer else None
+    if rope is not None:
+        kv = {} if fp8 else dict(k_cache=caches["k_cache"], v_cache=caches["v_cache"], k_new=new["k_new"],
+                                 v_new=new["v_new"])
+        if indexer:
+            kv.update(idx_k_cache=caches["idx_k_cache"], idx_k_new=new["idx_k_new"], idx_q=idx_q,
+                      idx_q_out=b.get("idx_q_rot"))
+        q, idx_q = msa_rope_append(shape, rope, tok_stream=tok[0], tok_pos=tok[1], q=q, q_pos=new["q_pos"],
+                                   q_out=b.get("q_rot"), stream=stream, pages=pages, **kv)
+    elif indexer:
+        append = msa_indexer_append_f16 if caches["idx_k_cache"].dtype == torch.float16 else msa_indexer_append
+        append(shape, caches["idx_k_cache"], new["idx_k_new"], *tok, stream, pages)
+    if fp8:
+        msa_kv_append_fp8(shape, caches["k_cache"], caches["v_cache"], caches["k_scale"], caches["v_scale"],
+                          new["k_new"], new["v_new"], *tok, rope, b.get("workspace_fp8"), stream, pages)
+    elif rope is None:
+        msa_kv_append(shape, caches["k_cache"], caches["v_cache"], new["k_new"], new["v_new"], *tok, stream, pages)
+    return q, idx_q
+
+
+def window_step(shape: Shape, caches: dict, new: dict, window: int, n_sink: int = 0, bufs: dict | None = None,
+                stream=None, prefill: bool = False, pages: Pages | None = None, rope: Rope | None = None):
+    """One step of a sliding-window layer through the C ABI: append the new
+    tokens' K/V rows and attend to the window and the sinks.
+
+    caches: k_cache, v_cache (bfloat16, or float8_e4m3fn with k_scale and
+    v_scale); new: tok_stream, tok_pos, k_new, v_new, q_stream, q_pos, q.
+    ``bufs`` may hold preallocated out / q_rot / workspace_fp8 / workspace.
+    With ``rope`` keys and queries arrive unrotated.  Returns out."""
+    b = bufs or {}
+    q, _ = _append_step(shape, caches, new, b, stream, pages, rope, False)
+    attend = msa_window_attn_prefill if prefill else msa_window_attn_decode
+    return attend(shape, q, caches["k_cache"], caches["v_cache"], new["q_stream"], new["q_pos"], window, n_sink, None,
+                  b.get("out"), b.get("workspace"), stream, pages, caches.get("k_scale"), caches.get("v_scale"))
 
 
 # ---- token-level variant (lightning indexer) --------------------------------
@@ -721,8 +1044,8 @@ class DecodeGraph:
     ``caches`` are updated in place by every replay."""
 
     def __init__(self, shape: Shape, caches: dict, inputs: dict, bufs: dict | None = None, prefill: bool = False,
-                 pages: Pages | None = None):
-        self.shape, self.caches, self.prefill, self.pages = shape, caches, prefill, pages
+                 pages: Pages | None = None, rope: Rope | None = None):
+        self.shape, self.caches, self.prefill, self.pages, self.rope = shape, caches, prefill, pages, rope
         dev = inputs["q"].device
         self._layout = []
         off = 0
@@ -750,12 +1073,12 @@ class DecodeGraph:
         side = torch.cuda.Stream(device=dev)
         side.wait_stream(torch.cuda.current_stream(dev))
         with torch.cuda.stream(side):                # first run outside the capture (one-time set-up)
-            decode_step(shape, caches, self.inputs, b, side, prefill, pages)
+            decode_step(shape, caches, self.inputs, b, side, prefill, pages, rope)
         torch.cuda.current_stream(dev).wait_stream(side)
         torch.cuda.synchronize(dev)
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
-            decode_step(shape, caches, self.inputs, b, None, prefill, pages)
+            decode_step(shape, caches, self.inputs, b, None, prefill, pages, rope)
 
     def host_buffer(self) -> torch.Tensor:
         """A pinned host buffer with the staging buffer's layout."""
@@ -798,9 +1121,9 @@ class StepPipeline:
     first inputs twice (one step per capture, as ``DecodeGraph`` does)."""
 
     def __init__(self, shape: Shape, caches: dict, inputs: dict, prefill: bool = False,
-                 pages: Pages | None = None):
+                 pages: Pages | None = None, rope: Rope | None = None):
         dev = inputs["q"].device
-        self.graphs = [DecodeGraph(shape, caches, inputs, None, prefill, pages) for _ in range(2)]
+        self.graphs = [DecodeGraph(shape, caches, inputs, None, prefill, pages, rope) for _ in range(2)]
         self.h2d = torch.cuda.Stream(device=dev)
         self.d2h = torch.cuda.Stream(device=dev)
         self.host_out = [torch.empty(g.out.shape, dtype=g.out.dtype).pin_memory() for g in self.graphs]

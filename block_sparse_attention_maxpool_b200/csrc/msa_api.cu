@@ -12,12 +12,14 @@
 
 #include "msa.h"
 #include "msa_append.cuh"
+#include "msa_attn_cluster.cuh"
 #include "msa_attn_decode_sk.cuh"
 #include "msa_attn_prefill_union.cuh"
 #include "msa_common.cuh"
 #include "msa_decode_fused.cuh"
 #include "msa_dsa_scores.cuh"
 #include "msa_dsa_select.cuh"
+#include "msa_rope_append.cuh"
 #include "msa_scores_gemv.cuh"
 #include "msa_scores_tc.cuh"
 #include "msa_select.cuh"
@@ -1060,6 +1062,352 @@ int msa_wait_selftest(long long wait_cycles, void* workspace, size_t workspace_b
   if (cudaLaunchKernelEx(&cfg, msa::fused::wait_selftest_kernel, bar, wait_cycles) != cudaSuccess)
     return MSA_ERR_CUDA;
   return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- rotating appends, 8-bit caches, window attention ---------------------------
+int rope_of(const msa_rope* r, msa::rope::Rope* out) {
+  out->inv_freq = nullptr;
+  out->half = 0;
+  out->interleaved = 0;
+  if (r == nullptr) return MSA_OK;
+  if (r->inv_freq == nullptr) return MSA_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(r->inv_freq) & 7u) != 0) return MSA_ERR_ALIGN;
+  if (r->rot_dim < 16 || r->rot_dim > 128 || r->rot_dim % 16 != 0) return MSA_ERR_SHAPE;
+  out->inv_freq = r->inv_freq;
+  out->half = r->rot_dim / 2;
+  out->interleaved = r->interleaved != 0;
+  return MSA_OK;
+}
+
+// A [rows][128] tensor of bytes; boxes of 128 rows x 128 bytes, 128-byte swizzle.
+int make_map_8bit(CUtensorMap* m, const void* base, int64_t rows) {
+  EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return MSA_ERR_CUDA;
+  const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, 128};
+  const cuuint32_t estride[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estride,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MSA_OK : MSA_ERR_CUDA;
+}
+
+size_t ext_attn_workspace(const msa_shape* sh, int32_t n_q, int mode) {
+  (void)sh;
+  (void)n_q;
+  (void)mode;
+  return 0;
+}
+
+// What a window or 8-bit attention call attends to.
+struct ExtAttn {
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;      // 8-bit cache
+  const float* v_scale;
+  bool f8;
+  const int32_t* sel;        // selection form, else window and n_sink
+  int window, n_sink;
+};
+
+// CTAs of one pair's cluster: a power of two, as many as keep the grid within
+// two CTAs per SM (what fits at once) and leave every CTA a unit.
+int cluster_ctas(int64_t n_pairs, int64_t units, int sms) {
+  int k = 1;
+  while (2 * k <= msa::cattn::kMaxCluster && 2 * k <= units && n_pairs * 2 * k <= 2 * static_cast<int64_t>(sms)) k *= 2;
+  return k;
+}
+
+template <bool kF8, bool kWin>
+int launch_cluster_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const msa::cattn::Params& P, int64_t n_pairs,
+                        int k, cudaStream_t s) {
+  const auto kernel = msa::cattn::attn_cluster_kernel<kF8, kWin>;
+  static std::atomic<uint64_t> smem_done{0};
+  static std::atomic<uint64_t> big_done{0};
+  int st = ensure_smem(kernel, msa::cattn::Layout::kBytes, smem_done);
+  if (st != MSA_OK) return st;
+  if (k > 8) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MSA_ERR_CUDA;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!(big_done.load(std::memory_order_acquire) & bit)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return MSA_ERR_CUDA;
+      big_done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n_pairs * k));
+  cfg.blockDim = dim3(msa::cattn::kThreads);
+  cfg.dynamicSmemBytes = msa::cattn::Layout::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = k;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = k > 1 ? 2 : 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, P, k));
+}
+
+int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, const ExtAttn& a, const int32_t* q_stream,
+             const int32_t* q_pos, int32_t n_q, float softmax_scale, msa_bf16* out, void* workspace,
+             size_t workspace_bytes, void* stream, int mode) {
+  int st = check_shape(sh);
+  if (st != MSA_OK) return st;
+  const bool win = a.window != 0;
+  if (n_q < 0) return MSA_ERR_RANGE;
+  if (n_q == 0) return MSA_OK;
+  if (!q || !a.k_cache || !a.v_cache || !q_stream || !q_pos || !out) return MSA_ERR_NULL;
+  if (a.f8 && (!a.k_scale || !a.v_scale)) return MSA_ERR_NULL;
+  if (!win && !a.sel) return MSA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(a.k_cache) || !aligned16(a.v_cache) || !aligned16(out)) return MSA_ERR_ALIGN;
+  if (a.f8 && (!aligned16(a.k_scale) || !aligned16(a.v_scale))) return MSA_ERR_ALIGN;
+  if (!win && !aligned16(a.sel)) return MSA_ERR_ALIGN;
+  if (!std::isfinite(softmax_scale)) return MSA_ERR_RANGE;
+  const int G = sh->n_kv_heads;
+  const int64_t n_pairs = static_cast<int64_t>(n_q) * G;
+  if (n_pairs * msa::cattn::kHpg >= (int64_t{1} << 31)) return MSA_ERR_RANGE;
+  msa::KvPages pg;
+  int64_t rows = 0;
+  if ((st = pages_of(sh, pages, &pg, &rows)) != MSA_OK) return st;
+  const size_t need = ext_attn_workspace(sh, n_q, mode);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return MSA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MSA_ERR_ALIGN;
+  }
+  int sms = 0;
+  if ((st = current_device_sms(&sms)) != MSA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CUtensorMap tm_k, tm_v;
+  for (int i = 0; i < 2; ++i) {
+    CUtensorMap* m = i == 0 ? &tm_k : &tm_v;
+    const void* base = i == 0 ? a.k_cache : a.v_cache;
+    st = a.f8 ? make_map_8bit(m, base, rows)
+              : make_map_16bit(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, msa::cattn::Unit<false>::kRows);
+    if (st != MSA_OK) return st;
+  }
+  msa::cattn::Params P;
+  P.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  P.q_stream = q_stream;
+  P.q_pos = q_pos;
+  P.sel = a.sel;
+  P.k_scale = a.k_scale;
+  P.v_scale = a.v_scale;
+  P.out = reinterpret_cast<__nv_bfloat16*>(out);
+  P.n_q = n_q;
+  P.G = G;
+  P.n_streams = sh->n_streams;
+  P.capacity = sh->capacity;
+  P.window = std::min(a.window, sh->capacity);
+  P.n_sink = std::min(a.n_sink, sh->capacity);
+  P.scale_log2 = softmax_scale * 1.4426950408889634f;
+  P.pages = pg;
+  const int64_t unit_rows = a.f8 ? msa::cattn::Unit<true>::kRows : msa::cattn::Unit<false>::kRows;
+  // the most units a query can have
+  const int64_t units = win ? std::min<int64_t>(sh->capacity / unit_rows, (P.window + unit_rows - 1) / unit_rows + 1 +
+                                                                              (P.n_sink + unit_rows - 1) / unit_rows)
+                            : msa::cattn::kTopK * (128 / unit_rows);
+  const int k = cluster_ctas(n_pairs, units, sms);
+  if (win)
+    return a.f8 ? launch_cluster_attn<true, true>(tm_k, tm_v, P, n_pairs, k, s)
+                : launch_cluster_attn<false, true>(tm_k, tm_v, P, n_pairs, k, s);
+  return launch_cluster_attn<true, false>(tm_k, tm_v, P, n_pairs, k, s);
+}
+
+int window_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, const void* k_cache,
+                const void* v_cache, bool f8, const float* k_scale, const float* v_scale, const int32_t* q_stream,
+                const int32_t* q_pos, int32_t n_q, int32_t window, int32_t n_sink, float softmax_scale, msa_bf16* out,
+                void* workspace, size_t workspace_bytes, void* stream, int mode) {
+  const int st = check_shape(sh);
+  if (st != MSA_OK) return st;
+  if (window < 1 || n_sink < 0) return MSA_ERR_RANGE;
+  const ExtAttn a{k_cache, v_cache, k_scale, v_scale, f8, nullptr, window, n_sink};
+  return ext_attn(sh, pages, q, a, q_stream, q_pos, n_q, softmax_scale, out, workspace, workspace_bytes, stream, mode);
+}
+
+}  // namespace
+
+extern "C" {
+
+int msa_rope_append(const msa_shape* shape, const msa_pages* pages, const msa_rope* rope, msa_bf16* k_cache,
+                    msa_bf16* v_cache, const msa_bf16* k_new, const msa_bf16* v_new, void* idx_k_cache,
+                    int32_t idx_k_f16, const float* idx_k_new, const int32_t* tok_stream, const int32_t* tok_pos,
+                    int32_t n_tok, const msa_bf16* q, msa_bf16* q_out, const float* idx_q, float* idx_q_out,
+                    const int32_t* q_pos, int32_t n_q, void* stream) {
+  int st = check_shape(shape);
+  if (st != MSA_OK) return st;
+  if (n_tok < 0 || n_q < 0) return MSA_ERR_RANGE;
+  msa::rope::AppendParams P;
+  if (rope == nullptr) return MSA_ERR_NULL;
+  if ((st = rope_of(rope, &P.rope)) != MSA_OK) return st;
+  const bool kv = k_cache || v_cache || k_new || v_new;
+  const bool idx = idx_k_cache || idx_k_new;
+  if (n_tok > 0) {
+    if (kv && (!k_cache || !v_cache || !k_new || !v_new)) return MSA_ERR_NULL;
+    if (idx && (!idx_k_cache || !idx_k_new)) return MSA_ERR_NULL;
+    if ((!kv && !idx) || !tok_stream || !tok_pos) return MSA_ERR_NULL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_new) || !aligned16(v_new) ||
+        !aligned16(idx_k_cache) || !aligned16(idx_k_new))
+      return MSA_ERR_ALIGN;
+  }
+  if (n_q > 0) {
+    if ((q == nullptr) != (q_out == nullptr) || (idx_q == nullptr) != (idx_q_out == nullptr)) return MSA_ERR_NULL;
+    if ((!q && !idx_q) || !q_pos) return MSA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(idx_q) || !aligned16(idx_q_out)) return MSA_ERR_ALIGN;
+  }
+  int64_t rows = 0;
+  if ((st = pages_of(shape, pages, &P.pages, &rows)) != MSA_OK) return st;
+  const int G = shape->n_kv_heads;
+  const int64_t units = (static_cast<int64_t>(n_tok) + n_q) * G;
+  if (units == 0) return MSA_OK;
+  if (units >= (int64_t{1} << 31)) return MSA_ERR_RANGE;
+  P.k_cache = reinterpret_cast<__nv_bfloat16*>(k_cache);
+  P.v_cache = reinterpret_cast<__nv_bfloat16*>(v_cache);
+  P.k_new = reinterpret_cast<const __nv_bfloat16*>(k_new);
+  P.v_new = reinterpret_cast<const __nv_bfloat16*>(v_new);
+  P.idx_cache = idx_k_cache;
+  P.idx_f16 = idx_k_f16 != 0;
+  P.idx_new = idx_k_new;
+  P.tok_stream = tok_stream;
+  P.tok_pos = tok_pos;
+  P.n_tok = n_tok;
+  P.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  P.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  P.idx_q = idx_q;
+  P.idx_q_out = idx_q_out;
+  P.q_pos = q_pos;
+  P.n_q = n_q;
+  P.n_streams = shape->n_streams;
+  P.G = G;
+  P.capacity = shape->capacity;
+  constexpr int kWarps = msa::rope::kWarps;
+  return cuda_status(launch(msa::rope::rope_append_kernel, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)),
+                            dim3(kWarps * 32), 0, static_cast<cudaStream_t>(stream), P));
+}
+
+size_t msa_kv_append_fp8_workspace_bytes(const msa_shape* shape, int32_t n_tok) {
+  if (check_shape(shape) != MSA_OK || n_tok < 0) return static_cast<size_t>(-1);
+  if (n_tok == 0) return 0;
+  return static_cast<size_t>(shape->n_streams) * (shape->capacity / 128) * shape->n_kv_heads *
+         sizeof(msa::rope::BlockNeed);
+}
+
+int msa_kv_append_fp8(const msa_shape* shape, const msa_pages* pages, const msa_rope* rope, msa_e4m3* k_cache,
+                      msa_e4m3* v_cache, float* k_scale, float* v_scale, const msa_bf16* k_new, const msa_bf16* v_new,
+                      const int32_t* tok_stream, const int32_t* tok_pos, int32_t n_tok, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int st = check_shape(shape);
+  if (st != MSA_OK) return st;
+  if (n_tok < 0) return MSA_ERR_RANGE;
+  msa::rope::Fp8Params P;
+  if ((st = rope_of(rope, &P.rope)) != MSA_OK) return st;
+  if (n_tok == 0) return MSA_OK;
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !k_new || !v_new || !tok_stream || !tok_pos)
+    return MSA_ERR_NULL;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) || !aligned16(k_new) ||
+      !aligned16(v_new))
+    return MSA_ERR_ALIGN;
+  int64_t rows = 0;
+  if ((st = pages_of(shape, pages, &P.pages, &rows)) != MSA_OK) return st;
+  const size_t need = msa_kv_append_fp8_workspace_bytes(shape, n_tok);
+  if (workspace == nullptr || workspace_bytes < need) return MSA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MSA_ERR_ALIGN;
+  const int G = shape->n_kv_heads;
+  const int64_t units = static_cast<int64_t>(n_tok) * G;
+  if (units >= (int64_t{1} << 31)) return MSA_ERR_RANGE;
+  P.k_cache = k_cache;
+  P.v_cache = v_cache;
+  P.k_scale = k_scale;
+  P.v_scale = v_scale;
+  P.k_new = reinterpret_cast<const __nv_bfloat16*>(k_new);
+  P.v_new = reinterpret_cast<const __nv_bfloat16*>(v_new);
+  P.tok_stream = tok_stream;
+  P.tok_pos = tok_pos;
+  P.n_tok = n_tok;
+  P.n_streams = shape->n_streams;
+  P.G = G;
+  P.capacity = shape->capacity;
+  P.need = static_cast<msa::rope::BlockNeed*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  constexpr int kWarps = msa::rope::kWarps;
+  const dim3 block(kWarps * 32);
+  const dim3 grid(static_cast<unsigned>((units + kWarps - 1) / kWarps));
+  const int64_t entries = static_cast<int64_t>(shape->n_streams) * (shape->capacity / 128) * G;
+  if (cudaMemsetAsync(workspace, 0, need, s) != cudaSuccess) return MSA_ERR_CUDA;
+  if (launch(msa::rope::fp8_need_kernel, grid, block, 0, s, P) != cudaSuccess) return MSA_ERR_CUDA;
+  if (launch(msa::rope::fp8_scale_kernel, dim3(static_cast<unsigned>((entries + kWarps * 32 - 1) / (kWarps * 32))),
+             block, 0, s, P) != cudaSuccess)
+    return MSA_ERR_CUDA;
+  return cuda_status(launch(msa::rope::fp8_store_kernel, grid, block, 0, s, P));
+}
+
+int msa_sparse_attn_decode_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                               const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
+                               const float* v_scale, const int32_t* sel, const int32_t* q_stream,
+                               const int32_t* q_pos, int32_t n_q, float softmax_scale, msa_bf16* out,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  const ExtAttn a{k_cache, v_cache, k_scale, v_scale, true, sel, 0, 0};
+  return ext_attn(shape, pages, q, a, q_stream, q_pos, n_q, softmax_scale, out, workspace, workspace_bytes, stream,
+                  MSA_MODE_DECODE);
+}
+
+int msa_sparse_attn_prefill_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                                const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
+                                const float* v_scale, const int32_t* sel, const int32_t* q_stream,
+                                const int32_t* q_pos, int32_t n_q, float softmax_scale, msa_bf16* out,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const ExtAttn a{k_cache, v_cache, k_scale, v_scale, true, sel, 0, 0};
+  return ext_attn(shape, pages, q, a, q_stream, q_pos, n_q, softmax_scale, out, workspace, workspace_bytes, stream,
+                  MSA_MODE_PREFILL);
+}
+
+int msa_window_attn_decode(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q, const msa_bf16* k_cache,
+                           const msa_bf16* v_cache, const int32_t* q_stream, const int32_t* q_pos, int32_t n_q,
+                           int32_t window, int32_t n_sink, float softmax_scale, msa_bf16* out, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  return window_attn(shape, pages, q, k_cache, v_cache, false, nullptr, nullptr, q_stream, q_pos, n_q, window, n_sink,
+                     softmax_scale, out, workspace, workspace_bytes, stream, MSA_MODE_DECODE);
+}
+
+int msa_window_attn_decode_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                               const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
+                               const float* v_scale, const int32_t* q_stream, const int32_t* q_pos, int32_t n_q,
+                               int32_t window, int32_t n_sink, float softmax_scale, msa_bf16* out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return window_attn(shape, pages, q, k_cache, v_cache, true, k_scale, v_scale, q_stream, q_pos, n_q, window, n_sink,
+                     softmax_scale, out, workspace, workspace_bytes, stream, MSA_MODE_DECODE);
+}
+
+int msa_window_attn_prefill(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                            const msa_bf16* k_cache, const msa_bf16* v_cache, const int32_t* q_stream,
+                            const int32_t* q_pos, int32_t n_q, int32_t window, int32_t n_sink, float softmax_scale,
+                            msa_bf16* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return window_attn(shape, pages, q, k_cache, v_cache, false, nullptr, nullptr, q_stream, q_pos, n_q, window, n_sink,
+                     softmax_scale, out, workspace, workspace_bytes, stream, MSA_MODE_PREFILL);
+}
+
+int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                                const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
+                                const float* v_scale, const int32_t* q_stream, const int32_t* q_pos, int32_t n_q,
+                                int32_t window, int32_t n_sink, float softmax_scale, msa_bf16* out, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  return window_attn(shape, pages, q, k_cache, v_cache, true, k_scale, v_scale, q_stream, q_pos, n_q, window, n_sink,
+                     softmax_scale, out, workspace, workspace_bytes, stream, MSA_MODE_PREFILL);
+}
+
+size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode) {
+  if (check_shape(shape) != MSA_OK || n_q < 0 || (mode != MSA_MODE_DECODE && mode != MSA_MODE_PREFILL))
+    return static_cast<size_t>(-1);
+  return ext_attn_workspace(shape, n_q, mode);
 }
 
 size_t msa_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode) {

@@ -416,6 +416,125 @@ MSA_API int msa_dsa_sparse_attn_decode(const msa_shape* shape, const msa_pages* 
                                        float softmax_scale, msa_bf16* out, void* workspace,
                                        size_t workspace_bytes, void* stream);
 
+/* ---- position rotation on the way into the cache --------------------------
+ * The calls above take keys and queries that were rotated already.  These
+ * rotate them: pair i of the first rot_dim dims of a row at position p turns
+ * by the angle p * inv_freq[i] (formed in float64),
+ *   (x0, x1) -> (x0 cos - x1 sin, x1 cos + x0 sin),
+ * pair i being dims (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved;
+ * later dims are copied.  Arithmetic in float32, one rounding to the stored
+ * type.  A token's position is its slot. */
+typedef struct msa_rope {
+  const double* inv_freq;   /* device, [rot_dim / 2], 8-byte aligned          */
+  int32_t rot_dim;          /* rotated dims: a multiple of 16, 16 .. 128      */
+  int32_t interleaved;      /* nonzero: pairs (2i, 2i + 1)                    */
+} msa_rope;
+
+/* msa_rope_append - a step's appends with the rotation applied on the way,
+ * and the step's queries rotated, in one launch:
+ *   k_cache, v_cache, k_new, v_new: as for msa_kv_append, K rows rotated (all
+ *     four NULL: no K/V rows, e.g. when they go to an 8-bit cache);
+ *   idx_k_cache, idx_k_new: as for msa_indexer_append (idx_k_f16 nonzero: an
+ *     fp16 cache, as for msa_indexer_append_f16), rotated (both NULL: none);
+ *   q [n_q][Hq][D] -> q_out, idx_q [n_q][G][Di] -> idx_q_out at positions
+ *     q_pos [n_q] (each pair may be NULL; an output may be its input).
+ * pages may be NULL (contiguous caches).  Tokens as for msa_kv_append: those
+ * with an out-of-range stream or slot are skipped (MSA_DEVERR_TOKEN_RANGE),
+ * those in an unmapped block too (MSA_DEVERR_PAGE_RANGE); two naming one
+ * slot race.  A query whose position is outside [0, capacity) is left
+ * unwritten and sets MSA_DEVERR_QUERY_RANGE.  n_tok and n_q may be 0. */
+MSA_API int msa_rope_append(const msa_shape* shape, const msa_pages* pages, const msa_rope* rope,
+                            msa_bf16* k_cache, msa_bf16* v_cache, const msa_bf16* k_new, const msa_bf16* v_new,
+                            void* idx_k_cache, int32_t idx_k_f16, const float* idx_k_new,
+                            const int32_t* tok_stream, const int32_t* tok_pos, int32_t n_tok,
+                            const msa_bf16* q, msa_bf16* q_out, const float* idx_q, float* idx_q_out,
+                            const int32_t* q_pos, int32_t n_q, void* stream);
+
+/* ---- 8-bit K/V caches -------------------------------------------------------
+ * K and V rows as e4m3 with one float32 scale per (128-token block, group)
+ * for K and one for V: a row stands for its e4m3 values times its block's
+ * scale.  Layouts: caches as the bf16 ones with one byte per value, scales
+ * [S][G][capacity / 128] (contiguous) or [n_pages][G] (pools).  Half the
+ * bytes of a bf16 cache. */
+typedef uint8_t msa_e4m3;
+
+/* msa_kv_append_fp8 - write new tokens' K and V rows ([n_tok][G][D] bf16),
+ * the K rows rotated when rope is not NULL, into an 8-bit cache.  For every
+ * (block, group) the call touches, and for K and V alike:
+ *   need  = the smallest power of two with |x| <= 448 need for every finite x
+ *           the call writes there (at least 2^-100);
+ *   after = max(before, need); before counts as empty when it is not
+ *           positive, or when the call writes the block's first slot (the
+ *           block starts anew, e.g. in a page that another sequence held);
+ *   rows already in the block are requantised from before to after when the
+ *   scale grows, the call's rows are quantised with after (each to the nearest
+ *   e4m3, ties to even; infinities become +-448, NaN stays NaN).
+ * So the result does not depend on the order of the tokens in the call.
+ * Other conditions as for msa_kv_append.  workspace: at least
+ * msa_kv_append_fp8_workspace_bytes(shape, n_tok) bytes, 16-byte aligned, its
+ * contents need not be initialised. */
+MSA_API int msa_kv_append_fp8(const msa_shape* shape, const msa_pages* pages, const msa_rope* rope,
+                              msa_e4m3* k_cache, msa_e4m3* v_cache, float* k_scale, float* v_scale,
+                              const msa_bf16* k_new, const msa_bf16* v_new, const int32_t* tok_stream,
+                              const int32_t* tok_pos, int32_t n_tok, void* workspace, size_t workspace_bytes,
+                              void* stream);
+/* Workspace bytes of msa_kv_append_fp8 ((size_t)-1: unsupported shape). */
+MSA_API size_t msa_kv_append_fp8_workspace_bytes(const msa_shape* shape, int32_t n_tok);
+
+/* msa_sparse_attn_decode_fp8, msa_sparse_attn_prefill_fp8 - the computation
+ * of msa_sparse_attn_decode over an 8-bit cache, for a few queries and for
+ * batches of many; same selection, layouts, rounding of the output and
+ * errors.  The products see the e4m3 values exactly; softmax, sums and the
+ * scales are float32.  pages may be NULL.  workspace: at least
+ * msa_attn_workspace_bytes(shape, n_q, mode) bytes, 16-byte aligned (NULL
+ * when that is 0). */
+MSA_API int msa_sparse_attn_decode_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                                       const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
+                                       const float* v_scale, const int32_t* sel, const int32_t* q_stream,
+                                       const int32_t* q_pos, int32_t n_q, float softmax_scale, msa_bf16* out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+MSA_API int msa_sparse_attn_prefill_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                                        const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
+                                        const float* v_scale, const int32_t* sel, const int32_t* q_stream,
+                                        const int32_t* q_pos, int32_t n_q, float softmax_scale, msa_bf16* out,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- sliding-window attention with sinks --------------------------------------
+ * For the layers of a model that see a window instead of selected blocks:
+ * out[i][h] = softmax(softmax_scale * q[i][h] . K_j) . V_j over the slots
+ * j <= q_pos[i] with j > q_pos[i] - window or j < n_sink (the first tokens,
+ * which stay visible).  window >= 1, n_sink >= 0; a window of at least the
+ * capacity is full causal attention.  Same caches, layouts, softmax, rounding
+ * and errors as msa_sparse_attn_decode; a visible block with no valid page is
+ * left out and sets MSA_DEVERR_PAGE_RANGE.  Rows outside the mask may hold
+ * anything.  The _fp8 calls read an 8-bit cache.  pages may be NULL.
+ * workspace: as for msa_sparse_attn_decode_fp8. */
+MSA_API int msa_window_attn_decode(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                                   const msa_bf16* k_cache, const msa_bf16* v_cache, const int32_t* q_stream,
+                                   const int32_t* q_pos, int32_t n_q, int32_t window, int32_t n_sink,
+                                   float softmax_scale, msa_bf16* out, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+MSA_API int msa_window_attn_decode_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                                       const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
+                                       const float* v_scale, const int32_t* q_stream, const int32_t* q_pos,
+                                       int32_t n_q, int32_t window, int32_t n_sink, float softmax_scale,
+                                       msa_bf16* out, void* workspace, size_t workspace_bytes, void* stream);
+MSA_API int msa_window_attn_prefill(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                                    const msa_bf16* k_cache, const msa_bf16* v_cache, const int32_t* q_stream,
+                                    const int32_t* q_pos, int32_t n_q, int32_t window, int32_t n_sink,
+                                    float softmax_scale, msa_bf16* out, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+MSA_API int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
+                                        const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
+                                        const float* v_scale, const int32_t* q_stream, const int32_t* q_pos,
+                                        int32_t n_q, int32_t window, int32_t n_sink, float softmax_scale,
+                                        msa_bf16* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that the window and 8-bit attention calls of `mode`
+ * (MSA_MODE_DECODE, MSA_MODE_PREFILL) need for n_q queries; (size_t)-1 for an
+ * unsupported shape. */
+MSA_API size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode);
+
 /* msa_decode_step_fused - one whole decode step in a single persistent
  * kernel: append the new tokens (msa_indexer_append + msa_kv_append), block
  * scores (msa_block_scores), top-16 (msa_select_topk) and block-sparse

@@ -1,0 +1,269 @@
+"""Sliding-window attention with sinks on the GPU against the float64 oracle: bf16 and 8-bit caches, contiguous and
+paged, single queries and batches, windows from one token to the whole cache, sinks before and inside the window."""
+import math
+
+import pytest
+import torch
+
+import block_sparse_attention_maxpool_b200 as msa
+from oracle import cache_ops as C
+from tests import parity_window as PW
+from tests.test_gpu_rope_append import freqs
+
+pytestmark = pytest.mark.gpu
+F8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from block_sparse_attention_maxpool_b200 import build as msa_build
+    msa_build.build()
+    msa.msa_get_device_error()
+
+
+def attend(mode, *a, **k):
+    return (msa.msa_window_attn_prefill if mode == "prefill" else msa.msa_window_attn_decode)(*a, **k)
+
+
+def make(S, G, cap, f8, gen):
+    """K and V: (as stored, scales or None, the float64 rows they stand for)."""
+    out = []
+    for _ in range(2):
+        x = torch.randn((S, G, cap, 128), generator=gen)
+        if f8:
+            x = x * torch.exp2(torch.randint(-3, 4, (S, G, cap // 128, 1, 1), generator=gen).float()).expand(
+                -1, -1, -1, 128, 1).reshape(S, G, cap, 1)
+            q8, sc = PW.quantise(x)
+            out.append((q8, sc, C.fp8_values(q8, sc)))
+        else:
+            out.append((x.bfloat16(), None, x.bfloat16().double()))
+    return out
+
+
+def run(mode, shape, q, kv, stream, pos, window, sink, table=None, n_pages=0, poison=True, scale=None, out=None):
+    """The call on device copies; every row that no query sees is NaN there."""
+    f8 = kv[0][1] is not None
+    args, scales = [], {}
+    for name, (x, sc, _) in zip("kv", kv):
+        raw = (x.view(torch.uint8) if f8 else x).clone()
+        if poison:
+            seen = torch.zeros(raw.shape[0], raw.shape[2], dtype=torch.bool)
+            for i in range(pos.numel()):
+                s, p = int(stream[i]), int(pos[i])
+                if 0 <= s < raw.shape[0] and 0 <= p < raw.shape[2]:
+                    seen[s, C.visible_slots(p, window, sink)] = True
+            raw.permute(0, 2, 1, 3)[~seen] = 0x7f if f8 else math.nan
+        if table is not None:
+            raw = PW.to_pool(raw, table, n_pages, 0x7f if f8 else math.nan)
+        args.append(raw.cuda().view(F8) if f8 else raw.cuda())
+        if f8:
+            scales[name + "_scale"] = (sc if table is None else PW.scale_pool(sc, table, n_pages)).cuda()
+    pages = None if table is None else msa.Pages(table.cuda(), n_pages)
+    return attend(mode, shape, q.cuda(), *args, stream.cuda(), pos.cuda(), window, sink, softmax_scale=scale, out=out,
+                  pages=pages, **scales)
+
+
+CASES = [
+    # S, G, cap, positions (stream, position), window, sink
+    (1, 4, 128, [(0, 0)], 1, 0),
+    (1, 1, 128, [(0, 127)], 1, 1),
+    (1, 4, 256, [(0, 200)], 64, 4),
+    (2, 4, 1024, [(0, 1023), (1, 511), (0, 63), (1, 64)], 300, 4),
+    (1, 2, 4096, [(0, 4095)], 4096, 0),
+    (1, 2, 2048, [(0, 2047), (0, 2000)], 1 << 30, 0),
+    (3, 1, 1536, [(2, 1500), (0, 7), (1, 900)], 129, 300),
+    (2, 16, 640, [(0, 600), (1, 601)], 100, 128),
+    (1, 4, 1024, [(0, p) for p in range(480, 560)], 200, 3),
+    (2, 2, 2048, [(s, p) for s in (0, 1) for p in range(900 + 7 * s, 1041)], 257, 129),
+    (4, 1, 768, [(s, p) for p in (5, 700, 300) for s in (3, 1, 2, 0)], 65, 0),
+    (2, 3, 896, [(i % 2, (37 * i) % 896) for i in range(70)], 150, 64),
+]
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_against_oracle(mode, f8, paged, case):
+    S, G, cap, at, window, sink = CASES[case]
+    gen = torch.Generator().manual_seed(1000 + case)
+    shape = msa.Shape(S, cap, 16 * G, G)
+    kv = make(S, G, cap, f8, gen)
+    stream, pos = (torch.tensor(x, dtype=torch.int32) for x in zip(*at))
+    q = (2 * torch.randn((len(at), 16 * G, 128), generator=gen)).bfloat16()
+    table, n_pages = PW.random_pages(S, cap // 128, 2, gen) if paged else (None, 0)
+    want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, window, sink, 128 ** -0.5)
+    got = run(mode, shape, q, kv, stream, pos, window, sink, table, n_pages)
+    PW.device_error()
+    PW.check_attention(got, want, spread, reach, PW.P_BF16)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("S,G,cap,window,sink", [(1, 1, 16384, 16000, 4), (2, 4, 8192, 5000, 100), (40, 4, 1024, 700, 4)])
+def test_long_windows_split_over_ctas(f8, S, G, cap, window, sink):
+    """One query per stream at odd places: every cluster size the host picks."""
+    gen = torch.Generator().manual_seed(S + cap)
+    shape = msa.Shape(S, cap, 16 * G, G)
+    kv = make(S, G, cap, f8, gen)
+    stream = torch.arange(S, dtype=torch.int32)
+    pos = torch.randint(cap // 2, cap, (S,), generator=gen).int()
+    q = torch.randn((S, 16 * G, 128), generator=gen).bfloat16()
+    want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, window, sink, 128 ** -0.5)
+    got = run("decode", shape, q, kv, stream, pos, window, sink)
+    again = run("decode", shape, q, kv, stream, pos, window, sink)
+    PW.device_error()
+    PW.check_attention(got, want, spread, reach, PW.P_BF16)
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("f8", [False, True])
+def test_steep_scores(mode, f8):
+    """Scores hundreds apart, the largest early, late and in the sinks, and a negative and a zero scale."""
+    gen = torch.Generator().manual_seed(77)
+    shape = msa.Shape(1, 1024, 16, 1)
+    kv = make(1, 1, 1024, f8, gen)
+    pos = torch.tensor([1023, 600, 300], dtype=torch.int32)
+    stream = torch.zeros(3, dtype=torch.int32)
+    q = (40 * torch.randn((3, 16, 128), generator=gen)).bfloat16()
+    for scale in (128 ** -0.5, -0.05, 0.0):
+        want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, 500, 10, scale)
+        got = run(mode, shape, q, kv, stream, pos, 500, 10, scale=scale)
+        PW.check_attention(got, want, spread, reach, PW.P_BF16)
+    PW.device_error()
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("f8", [False, True])
+def test_invalid_queries_and_unmapped_pages(mode, f8):
+    gen = torch.Generator().manual_seed(9)
+    S, G, cap = 2, 2, 640
+    shape = msa.Shape(S, cap, 32, G)
+    kv = make(S, G, cap, f8, gen)
+    table, n_pages = PW.random_pages(S, 5, 1, gen)
+    bad = table.clone()
+    bad[0, 3] = -1                   # inside the window of query 0
+    bad[1, 0] = n_pages              # the sinks of stream 1
+    bad[1, 1] = 1 << 30              # the window's first rows of query 5: 500 - 250 < j, j in block 1 is 251 .. 255
+    stream = torch.tensor([0, 2, -1, 0, 1, 1, 0], dtype=torch.int32)
+    pos = torch.tensor([600, 5, 5, 640, -7, 500, 3], dtype=torch.int32)
+    q = torch.randn((7, 32, 128), generator=gen).bfloat16()
+    window, sink = 250, 70
+    hidden = [(0, j) for j in range(384, 512)] + [(1, j) for j in range(0, 256)]
+    want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, window, sink, 128 ** -0.5, hidden)
+    out = torch.full((7, 32, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    args = []
+    for x, sc, _ in kv:
+        raw = x.view(torch.uint8) if f8 else x
+        pool = PW.to_pool(raw, table, n_pages, 0x7f if f8 else math.nan).cuda()
+        args.append((pool.view(F8) if f8 else pool, PW.scale_pool(sc, table, n_pages).cuda() if f8 else None))
+    attend(mode, shape, q.cuda(), args[0][0], args[1][0], stream.cuda(), pos.cuda(), window, sink, out=out,
+           pages=msa.Pages(bad.cuda(), n_pages), k_scale=args[0][1], v_scale=args[1][1])
+    PW.device_error(0x1 | 0x10)
+    PW.check_attention(out, want, spread, reach, PW.P_BF16)
+    assert not bool(out[[1, 2, 3, 4]].any())
+
+
+@pytest.mark.parametrize("prefill,f8", [(False, False), (True, False), (False, True), (True, True)])
+def test_window_steps_in_a_row(prefill, f8):
+    """Several steps of a local layer (append with rotation, then attention), on a stream of their own, and the last
+    one captured and replayed: each against the oracle on the caches it left."""
+    gen = torch.Generator().manual_seed(31)
+    S, G, cap, n_new = 3, 2, 1024, 33 if prefill else 1
+    shape = msa.Shape(S, cap, 32, G)
+    rope = msa.Rope(freqs(128, 1.0e4).cuda(), True)
+    table, n_pages = PW.random_pages(S, cap // 128, 1, gen)
+    pages = msa.Pages(table.cuda(), n_pages)
+    if f8:
+        c = msa.fp8_caches(shape, "cuda", n_pages)
+    else:
+        c = {k: torch.zeros((n_pages, G, 128, 128), dtype=torch.bfloat16, device="cuda") for k in ("k_cache", "v_cache")}
+    side = torch.cuda.Stream()
+    at = [0, 100, 500]
+
+    def logical():
+        out = []
+        for x in "kv":
+            pool = c[x + "_cache"].cpu()
+            pool = pool.double() * (c[x + "_scale"].cpu().double()[..., None, None] if f8 else 1.0)
+            out.append(torch.stack([torch.cat([pool[int(table[s, b])] for b in range(cap // 128)], 1) for s in range(S)]))
+        return out
+
+    def inputs():
+        stream = torch.arange(S).repeat_interleave(n_new).int()
+        pos = torch.cat([torch.arange(p, p + n_new) for p in at]).int()
+        n = S * n_new
+        d = dict(tok_stream=stream, tok_pos=pos, q_stream=stream, q_pos=pos,
+                 k_new=torch.randn((n, G, 128), generator=gen).bfloat16(),
+                 v_new=torch.randn((n, G, 128), generator=gen).bfloat16(),
+                 q=torch.randn((n, 32, 128), generator=gen).bfloat16())
+        return {k: v.cuda() for k, v in d.items()}
+
+    def check(out, new):
+        q, _ = msa.msa_rope_append(shape, rope, q=new["q"], q_pos=new["q_pos"])
+        k, v = logical()
+        want = C.window_attention(q.cpu(), k, v, new["q_stream"].cpu(), new["q_pos"].cpu(), 150, 20, 128 ** -0.5)
+        PW.check_attention(out, *want, PW.P_BF16)
+    for _ in range(3):
+        new = inputs()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            out = msa.window_step(shape, c, new, 150, 20, prefill=prefill, pages=pages, rope=rope)
+        torch.cuda.current_stream().wait_stream(side)
+        check(out, new)
+        at = [p + n_new for p in at]
+    new = inputs()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = msa.window_step(shape, c, new, 150, 20, prefill=prefill, pages=pages, rope=rope)
+    for _ in range(2):                       # the second replay appends the same rows again
+        graph.replay()
+        check(out, new)
+    # new contents in the captured buffers
+    at = [p + n_new for p in at]
+    for k, v in inputs().items():
+        new[k].copy_(v)
+    graph.replay()
+    check(out, new)
+    PW.device_error()
+
+
+def test_two_calls_at_once():
+    """Two decode calls on two streams share nothing."""
+    gen = torch.Generator().manual_seed(2)
+    shape = msa.Shape(1, 4096, 64, 4)
+    kv = make(1, 4, 4096, False, gen)
+    k, v = kv[0][0].cuda(), kv[1][0].cuda()
+    q = torch.randn((1, 64, 128), generator=gen).bfloat16().cuda()
+    zero, pos = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), 4000, dtype=torch.int32, device="cuda")
+    want = msa.msa_window_attn_decode(shape, q, k, v, zero, pos, 3000, 4)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(msa.msa_window_attn_decode(shape, q, k, v, zero, pos, 3000, 4))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got[0] + got[1])
+
+
+def test_large_offsets():
+    """A pool of more than 2^31 bytes: pages beyond 32-bit byte offsets."""
+    gen = torch.Generator().manual_seed(4)
+    G, n_pages = 16, 4500                               # 4500 * 16 * 128 * 256 B = 2.4 GB a cache
+    shape = msa.Shape(1, 512, 256, G)
+    k, v = (torch.zeros((n_pages, G, 128, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ids = torch.tensor([[n_pages - 1, 4400, 3, n_pages - 2]], dtype=torch.int32)
+    kl, vl = (torch.randn((1, G, 512, 128), generator=gen).bfloat16() for _ in range(2))
+    for b in range(4):
+        k[int(ids[0, b])], v[int(ids[0, b])] = kl[0, :, b * 128:b * 128 + 128].cuda(), vl[0, :, b * 128:b * 128 + 128].cuda()
+    q = torch.randn((2, 256, 128), generator=gen).bfloat16()
+    stream, pos = torch.zeros(2, dtype=torch.int32), torch.tensor([511, 400], dtype=torch.int32)
+    want = C.window_attention(q, kl, vl, stream, pos, 300, 4, 128 ** -0.5)
+    for mode in ("decode", "prefill"):
+        got = attend(mode, shape, q.cuda(), k, v, stream.cuda(), pos.cuda(), 300, 4, pages=msa.Pages(ids.cuda(), n_pages))
+        PW.check_attention(got, *want, PW.P_BF16)
+    PW.device_error()
