@@ -15,6 +15,7 @@
 #include "msa_attn_cluster.cuh"
 #include "msa_attn_decode_sk.cuh"
 #include "msa_attn_prefill_union.cuh"
+#include "msa_attn_tile.cuh"
 #include "msa_common.cuh"
 #include "msa_decode_fused.cuh"
 #include "msa_dsa_scores.cuh"
@@ -1158,6 +1159,24 @@ int launch_cluster_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const 
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, P, k));
 }
 
+// Prefill calls of at least this many (16-query tile, group) tasks take the
+// tensor-core tiles; fewer leave most SMs without a tile, and the cluster
+// kernel spreads them better.
+constexpr int64_t kMinTileTasks = 8;
+
+template <bool kF8, bool kWin>
+int launch_tile_attn(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                     const msa::tattn::Params& P, int sms, cudaStream_t s) {
+  const auto kernel = msa::tattn::attn_tile_kernel<kF8, kWin>;
+  static std::atomic<uint64_t> smem_done{0};
+  const int st = ensure_smem(kernel, msa::tattn::Layout<kF8>::kBytes, smem_done);
+  if (st != MSA_OK) return st;
+  const int64_t tasks = static_cast<int64_t>(P.G) * P.n_tiles;
+  return cuda_status(launch(kernel, dim3(static_cast<unsigned>(std::min<int64_t>(sms, tasks))),
+                            dim3(msa::tattn::Cfg<kF8>::kThreads), msa::tattn::Layout<kF8>::kBytes, s, tm_q, tm_k, tm_v,
+                            P));
+}
+
 int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, const ExtAttn& a, const int32_t* q_stream,
              const int32_t* q_pos, int32_t n_q, float softmax_scale, msa_bf16* out, void* workspace,
              size_t workspace_bytes, void* stream, int mode) {
@@ -1187,13 +1206,44 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   int sms = 0;
   if ((st = current_device_sms(&sms)) != MSA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int n_tiles = (n_q + msa::tattn::kTileQ - 1) / msa::tattn::kTileQ;
+  const bool tiles = mode == MSA_MODE_PREFILL && static_cast<int64_t>(n_tiles) * G >= kMinTileTasks;
   CUtensorMap tm_k, tm_v;
   for (int i = 0; i < 2; ++i) {
     CUtensorMap* m = i == 0 ? &tm_k : &tm_v;
     const void* base = i == 0 ? a.k_cache : a.v_cache;
     st = a.f8 ? make_map_8bit(m, base, rows)
-              : make_map_16bit(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, msa::cattn::Unit<false>::kRows);
+              : make_map_16bit(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows,
+                               tiles ? 128 : msa::cattn::Unit<false>::kRows);
     if (st != MSA_OK) return st;
+  }
+  const int window = std::min(a.window, sh->capacity);
+  const int n_sink = std::min(a.n_sink, sh->capacity);
+  if (tiles) {
+    CUtensorMap tm_q;
+    if ((st = make_map_16bit(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, n_pairs * msa::tattn::kHpg,
+                             msa::tattn::kHpg)) != MSA_OK)
+      return st;
+    msa::tattn::Params T;
+    T.q_stream = q_stream;
+    T.q_pos = q_pos;
+    T.sel = a.sel;
+    T.k_scale = a.k_scale;
+    T.v_scale = a.v_scale;
+    T.out = reinterpret_cast<__nv_bfloat16*>(out);
+    T.n_q = n_q;
+    T.G = G;
+    T.n_streams = sh->n_streams;
+    T.capacity = sh->capacity;
+    T.n_tiles = n_tiles;
+    T.window = window;
+    T.n_sink = n_sink;
+    T.scale_log2 = softmax_scale * 1.4426950408889634f;
+    T.pages = pg;
+    if (win)
+      return a.f8 ? launch_tile_attn<true, true>(tm_q, tm_k, tm_v, T, sms, s)
+                  : launch_tile_attn<false, true>(tm_q, tm_k, tm_v, T, sms, s);
+    return launch_tile_attn<true, false>(tm_q, tm_k, tm_v, T, sms, s);
   }
   msa::cattn::Params P;
   P.q = reinterpret_cast<const __nv_bfloat16*>(q);
@@ -1207,8 +1257,8 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   P.G = G;
   P.n_streams = sh->n_streams;
   P.capacity = sh->capacity;
-  P.window = std::min(a.window, sh->capacity);
-  P.n_sink = std::min(a.n_sink, sh->capacity);
+  P.window = window;
+  P.n_sink = n_sink;
   P.scale_log2 = softmax_scale * 1.4426950408889634f;
   P.pages = pg;
   const int64_t unit_rows = a.f8 ? msa::cattn::Unit<true>::kRows : msa::cattn::Unit<false>::kRows;
