@@ -20,6 +20,7 @@
 #include "msa_decode_fused.cuh"
 #include "msa_dsa_scores.cuh"
 #include "msa_dsa_select.cuh"
+#include "msa_fp8_expand.cuh"
 #include "msa_rope_append.cuh"
 #include "msa_scores_gemv.cuh"
 #include "msa_scores_tc.cuh"
@@ -1098,11 +1099,33 @@ int make_map_8bit(CUtensorMap* m, const void* base, int64_t rows) {
   return r == CUDA_SUCCESS ? MSA_OK : MSA_ERR_CUDA;
 }
 
-size_t ext_attn_workspace(const msa_shape* sh, int32_t n_q, int mode) {
-  (void)sh;
-  (void)n_q;
-  (void)mode;
-  return 0;
+// Prefill calls over an 8-bit cache expand it to bf16 first when a stream has
+// at least 64 queries on average; with fewer, the cluster kernel reads the
+// e4m3 rows directly.
+bool expands(const msa_shape* sh, int32_t n_q, int mode, bool f8) {
+  return f8 && mode == MSA_MODE_PREFILL && static_cast<int64_t>(n_q) >= int64_t{64} * std::min(sh->n_streams, n_q);
+}
+
+struct ExpandLayout {
+  size_t range, table, plans, k, v, total;
+};
+
+ExpandLayout expand_layout(const msa_shape* sh, int32_t n_q) {
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t blocks = static_cast<size_t>(sh->n_streams) * (sh->capacity / 128);
+  ExpandLayout l;
+  l.range = 0;
+  l.table = up(static_cast<size_t>(sh->n_streams) * 2 * sizeof(int32_t));
+  l.plans = up(l.table + blocks * sizeof(int32_t));
+  l.k = up(l.plans + attn_workspace(sh, n_q, MSA_MODE_PREFILL));
+  const size_t pool = blocks * sh->n_kv_heads * 128 * 128 * sizeof(msa_bf16);
+  l.v = l.k + pool;
+  l.total = l.v + pool;
+  return l;
+}
+
+size_t ext_attn_workspace(const msa_shape* sh, int32_t n_q, int mode, bool f8) {
+  return n_q > 0 && expands(sh, n_q, mode, f8) ? expand_layout(sh, n_q).total : 0;
 }
 
 // What a window or 8-bit attention call attends to.
@@ -1164,17 +1187,34 @@ int launch_cluster_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const 
 // kernel spreads them better.
 constexpr int64_t kMinTileTasks = 8;
 
-template <bool kF8, bool kWin>
-int launch_tile_attn(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                     const msa::tattn::Params& P, int sms, cudaStream_t s) {
-  const auto kernel = msa::tattn::attn_tile_kernel<kF8, kWin>;
+int tile_attn(const msa_shape* sh, const msa_bf16* q, const void* k, const void* v, const msa::KvPages& pg, int64_t rows,
+              const int32_t* q_stream, const int32_t* q_pos, int32_t n_q, int window, int n_sink, float softmax_scale,
+              msa_bf16* out, int sms, cudaStream_t s) {
+  CUtensorMap tm_q, tm_k, tm_v;
+  int st;
+  if ((st = make_kv_map(&tm_k, k, rows)) != MSA_OK) return st;
+  if ((st = make_kv_map(&tm_v, v, rows)) != MSA_OK) return st;
+  if ((st = make_map_16bit(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, static_cast<int64_t>(n_q) * sh->n_q_heads,
+                           msa::tattn::kHpg)) != MSA_OK)
+    return st;
   static std::atomic<uint64_t> smem_done{0};
-  const int st = ensure_smem(kernel, msa::tattn::Layout<kF8>::kBytes, smem_done);
-  if (st != MSA_OK) return st;
-  const int64_t tasks = static_cast<int64_t>(P.G) * P.n_tiles;
-  return cuda_status(launch(kernel, dim3(static_cast<unsigned>(std::min<int64_t>(sms, tasks))),
-                            dim3(msa::tattn::Cfg<kF8>::kThreads), msa::tattn::Layout<kF8>::kBytes, s, tm_q, tm_k, tm_v,
-                            P));
+  if ((st = ensure_smem(msa::tattn::attn_tile_kernel, msa::tattn::Layout::kBytes, smem_done)) != MSA_OK) return st;
+  msa::tattn::Params T;
+  T.q_stream = q_stream;
+  T.q_pos = q_pos;
+  T.out = reinterpret_cast<__nv_bfloat16*>(out);
+  T.n_q = n_q;
+  T.G = sh->n_kv_heads;
+  T.n_streams = sh->n_streams;
+  T.capacity = sh->capacity;
+  T.n_tiles = (n_q + msa::tattn::kTileQ - 1) / msa::tattn::kTileQ;
+  T.window = window;
+  T.n_sink = n_sink;
+  T.scale_log2 = softmax_scale * 1.4426950408889634f;
+  T.pages = pg;
+  const int64_t tasks = static_cast<int64_t>(T.G) * T.n_tiles;
+  return cuda_status(launch(msa::tattn::attn_tile_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(sms, tasks))),
+                            dim3(msa::tattn::kThreads), msa::tattn::Layout::kBytes, s, tm_q, tm_k, tm_v, T));
 }
 
 int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, const ExtAttn& a, const int32_t* q_stream,
@@ -1198,52 +1238,63 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   msa::KvPages pg;
   int64_t rows = 0;
   if ((st = pages_of(sh, pages, &pg, &rows)) != MSA_OK) return st;
-  const size_t need = ext_attn_workspace(sh, n_q, mode);
+  // (the selection tiles take a non-negative scale)
+  const size_t need = !win && softmax_scale < 0.f ? 0 : ext_attn_workspace(sh, n_q, mode, a.f8);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return MSA_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return MSA_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MSA_ERR_ALIGN;
   }
   int sms = 0;
   if ((st = current_device_sms(&sms)) != MSA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int n_tiles = (n_q + msa::tattn::kTileQ - 1) / msa::tattn::kTileQ;
-  const bool tiles = mode == MSA_MODE_PREFILL && static_cast<int64_t>(n_tiles) * G >= kMinTileTasks;
+  const int window = std::min(a.window, sh->capacity);
+  const int n_sink = std::min(a.n_sink, sh->capacity);
+  if (need > 0) {
+    const ExpandLayout l = expand_layout(sh, n_q);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    msa::expand::Params E;
+    E.k_cache = static_cast<const uint8_t*>(a.k_cache);
+    E.v_cache = static_cast<const uint8_t*>(a.v_cache);
+    E.k_scale = a.k_scale;
+    E.v_scale = a.v_scale;
+    E.k_out = reinterpret_cast<uint4*>(ws + l.k);
+    E.v_out = reinterpret_cast<uint4*>(ws + l.v);
+    E.table = reinterpret_cast<int32_t*>(ws + l.table);
+    E.range = reinterpret_cast<int32_t*>(ws + l.range);
+    E.q_stream = q_stream;
+    E.q_pos = q_pos;
+    E.n_q = n_q;
+    E.G = G;
+    E.n_streams = sh->n_streams;
+    E.capacity = sh->capacity;
+    E.window = win ? window : sh->capacity;
+    E.n_sink = n_sink;
+    E.pages = pg;
+    const int64_t blocks = static_cast<int64_t>(sh->n_streams) * (sh->capacity / 128);
+    if (cudaMemsetAsync(E.range, 0, static_cast<size_t>(sh->n_streams) * 2 * sizeof(int32_t), s) != cudaSuccess)
+      return MSA_ERR_CUDA;
+    if (launch(msa::expand::expand_range_kernel, dim3((n_q + 255) / 256), dim3(256), 0, s, E) != cudaSuccess ||
+        launch(msa::expand::expand_kernel, dim3(static_cast<unsigned>(blocks * G)), dim3(256), 0, s, E) != cudaSuccess)
+      return MSA_ERR_CUDA;
+    const msa_pages mine{E.table, static_cast<int32_t>(blocks)};
+    if (!win)
+      return sparse_attn(sh, q, reinterpret_cast<const msa_bf16*>(E.k_out), reinterpret_cast<const msa_bf16*>(E.v_out),
+                         a.sel, q_stream, q_pos, n_q, softmax_scale, out, ws + l.plans, l.k - l.plans, stream,
+                         MSA_MODE_PREFILL, &mine);
+    return tile_attn(sh, q, E.k_out, E.v_out, msa::KvPages{E.table, static_cast<int>(blocks)}, blocks * G * 128,
+                     q_stream, q_pos, n_q, window, n_sink, softmax_scale, out, sms, s);
+  }
+  const int64_t tile_tasks = (static_cast<int64_t>(n_q) + msa::tattn::kTileQ - 1) / msa::tattn::kTileQ * G;
+  if (mode == MSA_MODE_PREFILL && !a.f8 && tile_tasks >= kMinTileTasks)
+    return tile_attn(sh, q, a.k_cache, a.v_cache, pg, rows, q_stream, q_pos, n_q, window, n_sink, softmax_scale, out,
+                     sms, s);
   CUtensorMap tm_k, tm_v;
   for (int i = 0; i < 2; ++i) {
     CUtensorMap* m = i == 0 ? &tm_k : &tm_v;
     const void* base = i == 0 ? a.k_cache : a.v_cache;
     st = a.f8 ? make_map_8bit(m, base, rows)
-              : make_map_16bit(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows,
-                               tiles ? 128 : msa::cattn::Unit<false>::kRows);
+              : make_map_16bit(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, msa::cattn::Unit<false>::kRows);
     if (st != MSA_OK) return st;
-  }
-  const int window = std::min(a.window, sh->capacity);
-  const int n_sink = std::min(a.n_sink, sh->capacity);
-  if (tiles) {
-    CUtensorMap tm_q;
-    if ((st = make_map_16bit(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, n_pairs * msa::tattn::kHpg,
-                             msa::tattn::kHpg)) != MSA_OK)
-      return st;
-    msa::tattn::Params T;
-    T.q_stream = q_stream;
-    T.q_pos = q_pos;
-    T.sel = a.sel;
-    T.k_scale = a.k_scale;
-    T.v_scale = a.v_scale;
-    T.out = reinterpret_cast<__nv_bfloat16*>(out);
-    T.n_q = n_q;
-    T.G = G;
-    T.n_streams = sh->n_streams;
-    T.capacity = sh->capacity;
-    T.n_tiles = n_tiles;
-    T.window = window;
-    T.n_sink = n_sink;
-    T.scale_log2 = softmax_scale * 1.4426950408889634f;
-    T.pages = pg;
-    if (win)
-      return a.f8 ? launch_tile_attn<true, true>(tm_q, tm_k, tm_v, T, sms, s)
-                  : launch_tile_attn<false, true>(tm_q, tm_k, tm_v, T, sms, s);
-    return launch_tile_attn<true, false>(tm_q, tm_k, tm_v, T, sms, s);
   }
   msa::cattn::Params P;
   P.q = reinterpret_cast<const __nv_bfloat16*>(q);
@@ -1454,10 +1505,10 @@ int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages* pages, 
                      softmax_scale, out, workspace, workspace_bytes, stream, MSA_MODE_PREFILL);
 }
 
-size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode) {
+size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode, int32_t fp8) {
   if (check_shape(shape) != MSA_OK || n_q < 0 || (mode != MSA_MODE_DECODE && mode != MSA_MODE_PREFILL))
     return static_cast<size_t>(-1);
-  return ext_attn_workspace(shape, n_q, mode);
+  return ext_attn_workspace(shape, n_q, mode, fp8 != 0);
 }
 
 size_t msa_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode) {

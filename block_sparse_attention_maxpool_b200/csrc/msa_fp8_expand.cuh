@@ -1,0 +1,116 @@
+// Expansion of an 8-bit cache to bf16, ahead of a prefill call's attention.
+//
+// A prompt's tiles read a block many times (every 16 queries of a window read
+// it again, 8 queries of a selection share it at best), so the e4m3 values
+// are converted once per call, by a kernel of their own, into page pools in
+// the caller's workspace that the bf16 prefill kernels read through a page
+// table made here: bf16(scale * e4m3), exact when the scale is a power of
+// two, as the append writes it.  Only blocks that some query of the call can
+// see are touched.  Bound by bytes: 128 read and 256 written per row.
+// (Converted inside the attention kernel by four warps of its own, block by
+// block, the 2048-query selection on 16384 tokens took 1.04 ms and a window
+// of 1000 over 2 x 2001 queries 0.176 ms: the conversion of a block, about
+// 4000 cycles next to the softmax warps, paced the loop.)
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "msa_common.cuh"
+
+namespace msa {
+namespace expand {
+
+struct Params {
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale;       // scale of cache row r: k_scale[r / 128]
+  const float* v_scale;
+  uint4* k_out;               // [S * nblk][G][128][128] bf16
+  uint4* v_out;
+  int32_t* table;             // [S][nblk]: the expanded block's page, -1 without one
+  int32_t* range;             // [S][2], zeroed: highest position + 1, capacity - lowest slot seen
+  const int32_t* q_stream;
+  const int32_t* q_pos;
+  int n_q, G, n_streams, capacity;
+  int window, n_sink;         // selection form: window = capacity, n_sink = 0
+  KvPages pages;
+};
+
+// The slots that each stream's queries can see.
+__global__ void __launch_bounds__(256) expand_range_kernel(const Params P) {
+  pdl_trigger();
+  pdl_wait();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  int s = -1, p = 0;
+  if (i < P.n_q) {
+    s = P.q_stream[i];
+    p = P.q_pos[i];
+    if (s < 0 || s >= P.n_streams || p < 0 || p >= P.capacity) s = -1;
+  }
+  const unsigned same = __match_any_sync(0xffffffffu, s);
+  const unsigned hi = __reduce_max_sync(same, static_cast<unsigned>(p + 1));
+  const unsigned lo = __reduce_max_sync(same, static_cast<unsigned>(P.capacity - max(0, p - P.window + 1)));
+  if (s >= 0 && (threadIdx.x & 31) == __ffs(same) - 1) {
+    atomicMax(P.range + 2 * s, static_cast<int>(hi));
+    atomicMax(P.range + 2 * s + 1, static_cast<int>(lo));
+  }
+}
+
+// 16 e4m3 values times `f`, as bf16.
+__device__ __forceinline__ void expand16(const uint4& x, float f, uint4& a, uint4& b) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w[i >> 1] >> ((i & 1) * 16))));
+    const float2 v = __half22float2(*reinterpret_cast<__half2*>(&h));
+    r[i] = pack_bf16(v.x * f, v.y * f);
+  }
+  a = make_uint4(r[0], r[1], r[2], r[3]);
+  b = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// One CTA per (stream, block, group).
+__global__ void __launch_bounds__(256) expand_kernel(const Params P) {
+  pdl_trigger();
+  pdl_wait();
+  const int nblk = P.capacity / 128;
+  const long long sb = blockIdx.x / P.G;
+  const int g = static_cast<int>(blockIdx.x - sb * P.G);
+  const int s = static_cast<int>(sb / nblk), b = static_cast<int>(sb - static_cast<long long>(s) * nblk);
+  const int hi = P.range[2 * s], first = P.capacity - P.range[2 * s + 1];
+  const int j0 = b * 128;
+  if (j0 >= hi || (j0 + 127 < first && j0 >= P.n_sink)) return;   // nobody looks at its table entry either
+  const long long row = kv_block_row(P.pages, s, g, b, P.G, P.capacity);
+  if (g == 0 && threadIdx.x == 0) P.table[sb] = row < 0 ? -1 : static_cast<int32_t>(sb);
+  if (row < 0) return;
+  const float ks = P.k_scale[row / 128], vs = P.v_scale[row / 128];
+  const uint4* k = reinterpret_cast<const uint4*>(P.k_cache + row * 128);
+  const uint4* v = reinterpret_cast<const uint4*>(P.v_cache + row * 128);
+  uint4* ko = P.k_out + (sb * P.G + g) * (128 * 16);
+  uint4* vo = P.v_out + (sb * P.G + g) * (128 * 16);
+  uint4 x[4], y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = __ldg(k + threadIdx.x + 256 * i);
+    y[i] = __ldg(v + threadIdx.x + 256 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // rows that nobody sees become zeros (they may hold NaN)
+    const int j = j0 + (threadIdx.x + 256 * i) / 8;
+    if (j >= hi || (j < first && j >= P.n_sink)) x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int at = (threadIdx.x + 256 * i) * 2;
+    uint4 a, c;
+    expand16(x[i], ks, a, c);
+    ko[at] = a;
+    ko[at + 1] = c;
+    expand16(y[i], vs, a, c);
+    vo[at] = a;
+    vo[at + 1] = c;
+  }
+}
+
+}  // namespace expand
+}  // namespace msa

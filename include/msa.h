@@ -485,9 +485,11 @@ MSA_API size_t msa_kv_append_fp8_workspace_bytes(const msa_shape* shape, int32_t
  * of msa_sparse_attn_decode over an 8-bit cache, for a few queries and for
  * batches of many; same selection, layouts, rounding of the output and
  * errors.  The products see the e4m3 values exactly; softmax, sums and the
- * scales are float32.  pages may be NULL.  workspace: at least
- * msa_attn_workspace_bytes(shape, n_q, mode) bytes, 16-byte aligned (NULL
- * when that is 0). */
+ * scales are float32.  The prefill call takes scale * e4m3 as bf16 when it
+ * expands the cache (see msa_attn_workspace_bytes): exact for scales that are
+ * powers of two, as msa_kv_append_fp8 writes them, else one more rounding.
+ * pages may be NULL.  workspace: at least msa_attn_workspace_bytes(shape,
+ * n_q, mode, 1) bytes, 256-byte aligned (NULL when that is 0). */
 MSA_API int msa_sparse_attn_decode_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
                                        const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
                                        const float* v_scale, const int32_t* sel, const int32_t* q_stream,
@@ -506,9 +508,13 @@ MSA_API int msa_sparse_attn_prefill_fp8(const msa_shape* shape, const msa_pages*
  * which stay visible).  window >= 1, n_sink >= 0; a window of at least the
  * capacity is full causal attention.  Same caches, layouts, softmax, rounding
  * and errors as msa_sparse_attn_decode; a visible block with no valid page is
- * left out and sets MSA_DEVERR_PAGE_RANGE.  Rows outside the mask may hold
- * anything.  The _fp8 calls read an 8-bit cache.  pages may be NULL.
- * workspace: as for msa_sparse_attn_decode_fp8. */
+ * left out and sets MSA_DEVERR_PAGE_RANGE.  Rows that no query of the call
+ * sees may hold anything.  (In the prefill calls a NaN or infinity in a V row
+ * that a query sees can reach the other queries of its tile of 16.)  The _fp8
+ * calls read an 8-bit cache, as msa_sparse_attn_decode_fp8 and
+ * msa_sparse_attn_prefill_fp8 do.  pages may be NULL.  workspace: at least
+ * msa_attn_workspace_bytes(shape, n_q, mode, fp8) bytes, 256-byte aligned
+ * (NULL when that is 0). */
 MSA_API int msa_window_attn_decode(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
                                    const msa_bf16* k_cache, const msa_bf16* v_cache, const int32_t* q_stream,
                                    const int32_t* q_pos, int32_t n_q, int32_t window, int32_t n_sink,
@@ -531,9 +537,13 @@ MSA_API int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages*
                                         msa_bf16* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace that the window and 8-bit attention calls of `mode`
- * (MSA_MODE_DECODE, MSA_MODE_PREFILL) need for n_q queries; (size_t)-1 for an
- * unsupported shape. */
-MSA_API size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode);
+ * (MSA_MODE_DECODE, MSA_MODE_PREFILL) need for n_q queries over a bf16 or
+ * (fp8 nonzero) an 8-bit cache; (size_t)-1 for an unsupported shape.  It is 0
+ * except for prefill calls over an 8-bit cache with at least 64 queries per
+ * stream on average: those expand the blocks that the call's queries can see
+ * to bf16 in the workspace, which has room for the whole cache (512 bytes per
+ * slot and group; one buffer serves all layers of a model in turn). */
+MSA_API size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode, int32_t fp8);
 
 /* msa_decode_step_fused - one whole decode step in a single persistent
  * kernel: append the new tokens (msa_indexer_append + msa_kv_append), block

@@ -24,9 +24,13 @@ P_BF16, P_FP16 = 2.0 ** -8, 2.0 ** -11
 POISON = float("nan")
 
 
-def check_attention(got, want, spread, reach, p_round):
-    d = p_round + 2 * (138 * U) * reach + 2.0 ** -18
+def check_attention(got, want, spread, reach, p_round, kv_round=0.0):
+    """kv_round: rounding of the K and V values themselves (2^-8 where an 8-bit cache with scales that are no powers
+    of two is expanded to bf16): a score moves by kv_round times ``reach`` at most, out by kv_round sum_j w_j |v_j|,
+    which is at most spread + |out|."""
+    d = p_round + 2 * (138 * U + kv_round) * reach + 2.0 ** -18
     tol = d / (1 - d).clamp_min(0.5) * spread + 2.0 ** -8 * want.abs() * (1 + 2.0 ** -7) + 1e-30
+    tol = tol + kv_round * (spread + want.abs())
     g = got.double().cpu()
     assert bool(g.isfinite().all()), "not finite"
     err = (g - want).abs()

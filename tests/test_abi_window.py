@@ -80,10 +80,11 @@ def test_fp8_append_refusals(lib):
 @pytest.mark.parametrize("mode", ["decode", "prefill"])
 def test_attention_refusals(lib, mode):
     m = msa.MODE_PREFILL if mode == "prefill" else msa.MODE_DECODE
-    need = lib.msa_attn_workspace_bytes(GOOD.c(), 2, m)
-    assert lib.msa_attn_workspace_bytes(BAD.c(), 2, m) == ctypes.c_size_t(-1).value
-    assert lib.msa_attn_workspace_bytes(GOOD.c(), -2, m) == ctypes.c_size_t(-1).value
-    assert lib.msa_attn_workspace_bytes(GOOD.c(), 2, 2) == ctypes.c_size_t(-1).value
+    need = lib.msa_attn_workspace_bytes(GOOD.c(), 2, m, 1)
+    assert need == lib.msa_attn_workspace_bytes(GOOD.c(), 200, m, 0) == 0
+    assert lib.msa_attn_workspace_bytes(BAD.c(), 2, m, 0) == ctypes.c_size_t(-1).value
+    assert lib.msa_attn_workspace_bytes(GOOD.c(), -2, m, 0) == ctypes.c_size_t(-1).value
+    assert lib.msa_attn_workspace_bytes(GOOD.c(), 2, 2, 1) == ctypes.c_size_t(-1).value
     scale = ctypes.c_float(0.1)
     for f8 in (False, True):
         fn = getattr(lib, f"msa_window_attn_{mode}" + ("_fp8" if f8 else ""))
@@ -109,10 +110,13 @@ def test_attention_refusals(lib, mode):
             assert call(kv=tuple(FAKE + 4 if j == i else FAKE for j in range(nkv))) == -2
         assert call(pages=msa.CPages(FAKE, -1)) == -4
         assert call(n=1 << 26, shape=msa.Shape(1, 128, 256, 16)) == -4
-        if need:
-            assert call(ws=0) == -5
-            assert call(wb=need - 1) == -5
-            assert call(ws=FAKE + 8) == -2
+        if f8 and mode == "prefill":           # 64 queries per stream: the cache is expanded to bf16
+            big = lib.msa_attn_workspace_bytes(GOOD.c(), 128, m, 1)
+            assert big >= 2 * 4 * 1024 * 512
+            assert lib.msa_attn_workspace_bytes(GOOD.c(), 127, m, 1) == 0
+            assert call(n=128, ws=0, wb=big) == -5
+            assert call(n=128, wb=big - 1) == -5
+            assert call(n=128, ws=FAKE + 128, wb=big) == -2
     fn = getattr(lib, f"msa_sparse_attn_{mode}_fp8")
 
     def sparse(shape=GOOD, q=FAKE, kv=(FAKE,) * 4, sel=FAKE, n=2, sc=scale, ws=FAKE, wb=need):

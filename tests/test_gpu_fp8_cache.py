@@ -188,6 +188,8 @@ def random_sel(n, G, pos, gen, nblk):
     (5, 2, 2176, 37, False, False),
     (2, 16, 640, 9, True, True),
     (1, 4, 2944, 150, True, True),
+    (2, 2, 2560, 300, False, False),
+    (3, 1, 1024, 500, True, True),
 ])
 def test_selected_attention(mode, S, G, cap, n, paged, pow2):
     gen = torch.Generator().manual_seed(S * cap + n)
@@ -223,7 +225,8 @@ def test_selected_attention(mode, S, G, cap, n, paged, pow2):
              pos.cuda(), out=out, pages=pages)
     assert got is out
     PW.device_error()
-    print(f"\n[fp8 {mode}] of its bound: {PW.check_attention(got, want, spread, reach, PW.P_BF16):.2f}")
+    kv_round = 2.0 ** -8 if mode == "prefill" and not pow2 and n >= 64 * S else 0.0
+    print(f"\n[fp8 {mode}] of its bound: {PW.check_attention(got, want, spread, reach, PW.P_BF16, kv_round):.2f}")
 
 
 @pytest.mark.parametrize("mode", ["decode", "prefill"])
@@ -234,15 +237,17 @@ def test_nothing_to_attend(mode):
     k8, ks = PW.quantise(torch.randn((3, 1, 128, 128), generator=gen))
     table = torch.tensor([[0, -1, 1, 2], [3, -2, 0, 1]], dtype=torch.int32)
     pages = msa.Pages(table.cuda(), 3)
-    stream = torch.tensor([0, 2, -1, 0, 0, 0, 1], dtype=torch.int32)
-    pos = torch.tensor([511, 5, 5, 512, -1, 200, 130], dtype=torch.int32)
+    times = 30 if mode == "prefill" else 1
+    stream = torch.tensor([0, 2, -1, 0, 0, 0, 1] * times, dtype=torch.int32)
+    pos = torch.tensor([511, 5, 5, 512, -1, 200, 130] * times, dtype=torch.int32)
     sel = torch.full((7, 1, 16), -1, dtype=torch.int32)
     sel[1:5, 0, 0] = 0
     sel[5, 0, :2] = torch.tensor([1, 3])            # unmapped, and past the query
     sel[6, 0, :2] = torch.tensor([0, 1])            # page 3 of 3, and -2
+    sel = sel.repeat(times, 1, 1)
     fn = msa.msa_sparse_attn_prefill_fp8 if mode == "prefill" else msa.msa_sparse_attn_decode_fp8
-    out = torch.full((7, 16, 128), math.nan, dtype=torch.bfloat16, device="cuda")
-    q = torch.randn((7, 16, 128), generator=gen).bfloat16().cuda()
+    out = torch.full((7 * times, 16, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    q = torch.randn((7 * times, 16, 128), generator=gen).bfloat16().cuda()
     fn(shape, q, k8.cuda(), k8.cuda(), ks.view(3, 1).cuda(), ks.view(3, 1).cuda(), sel.cuda(), stream.cuda(),
        pos.cuda(), out=out, pages=pages)
     PW.device_error(0x1 | 0x4 | 0x10)
@@ -254,7 +259,7 @@ def test_decode_step_on_8bit_caches(prefill):
     """decode_step with 8-bit caches and rotation: the selection of the bf16 step's scores, attention within the bound
     of the oracle on the caches the step left; captured and replayed it gives the same bits."""
     gen = torch.Generator().manual_seed(21)
-    S, G, cap, new_n = 2, 2, 2560, 40 if prefill else 1
+    S, G, cap, new_n = 2, 2, 2560, 70 if prefill else 1
     shape = msa.Shape(S, cap, 32, G)
     rope = msa.Rope(freqs(64).cuda())
     had = caches(S, G, cap, gen, spread=False)

@@ -79,6 +79,7 @@ CASES = [
     (2, 2, 2048, [(s, p) for s in (0, 1) for p in range(900 + 7 * s, 1041)], 257, 129),
     (4, 1, 768, [(s, p) for p in (5, 700, 300) for s in (3, 1, 2, 0)], 65, 0),
     (2, 3, 896, [(i % 2, (37 * i) % 896) for i in range(70)], 150, 64),
+    (2, 2, 896, [(i % 2, (37 * i) % 896) for i in range(150)], 150, 64),
 ]
 
 
@@ -125,9 +126,10 @@ def test_steep_scores(mode, f8):
     gen = torch.Generator().manual_seed(77)
     shape = msa.Shape(1, 1024, 16, 1)
     kv = make(1, 1, 1024, f8, gen)
-    pos = torch.tensor([1023, 600, 300], dtype=torch.int32)
-    stream = torch.zeros(3, dtype=torch.int32)
-    q = (40 * torch.randn((3, 16, 128), generator=gen)).bfloat16()
+    n = 140 if mode == "prefill" else 3
+    pos = torch.cat((torch.tensor([1023, 600, 300]), torch.arange(700, 700 + n - 3))).int()
+    stream = torch.zeros(n, dtype=torch.int32)
+    q = (40 * torch.randn((n, 16, 128), generator=gen)).bfloat16()
     for scale in (128 ** -0.5, -0.05, 0.0):
         want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, 500, 10, scale)
         got = run(mode, shape, q, kv, stream, pos, 500, 10, scale=scale)
@@ -147,13 +149,15 @@ def test_invalid_queries_and_unmapped_pages(mode, f8):
     bad[0, 3] = -1                   # inside the window of query 0
     bad[1, 0] = n_pages              # the sinks of stream 1
     bad[1, 1] = 1 << 30              # the window's first rows of query 5: 500 - 250 < j, j in block 1 is 251 .. 255
-    stream = torch.tensor([0, 2, -1, 0, 1, 1, 0], dtype=torch.int32)
-    pos = torch.tensor([600, 5, 5, 640, -7, 500, 3], dtype=torch.int32)
-    q = torch.randn((7, 32, 128), generator=gen).bfloat16()
+    times = 20 if mode == "prefill" else 1
+    stream = torch.tensor([0, 2, -1, 0, 1, 1, 0] * times, dtype=torch.int32)
+    pos = torch.tensor([600, 5, 5, 640, -7, 500, 3] * times, dtype=torch.int32)
+    n = 7 * times
+    q = torch.randn((n, 32, 128), generator=gen).bfloat16()
     window, sink = 250, 70
     hidden = [(0, j) for j in range(384, 512)] + [(1, j) for j in range(0, 256)]
     want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, window, sink, 128 ** -0.5, hidden)
-    out = torch.full((7, 32, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((n, 32, 128), math.nan, dtype=torch.bfloat16, device="cuda")
     args = []
     for x, sc, _ in kv:
         raw = x.view(torch.uint8) if f8 else x
@@ -163,7 +167,7 @@ def test_invalid_queries_and_unmapped_pages(mode, f8):
            pages=msa.Pages(bad.cuda(), n_pages), k_scale=args[0][1], v_scale=args[1][1])
     PW.device_error(0x1 | 0x10)
     PW.check_attention(out, want, spread, reach, PW.P_BF16)
-    assert not bool(out[[1, 2, 3, 4]].any())
+    assert not bool(out[(stream < 0) | (stream > 1) | (pos < 0) | (pos >= cap)].any())
 
 
 @pytest.mark.parametrize("prefill,f8", [(False, False), (True, False), (False, True), (True, True)])
@@ -171,7 +175,7 @@ def test_window_steps_in_a_row(prefill, f8):
     """Several steps of a local layer (append with rotation, then attention), on a stream of their own, and the last
     one captured and replayed: each against the oracle on the caches it left."""
     gen = torch.Generator().manual_seed(31)
-    S, G, cap, n_new = 3, 2, 1024, 33 if prefill else 1
+    S, G, cap, n_new = 3, 2, 1024, 65 if prefill else 1
     shape = msa.Shape(S, cap, 32, G)
     rope = msa.Rope(freqs(128, 1.0e4).cuda(), True)
     table, n_pages = PW.random_pages(S, cap // 128, 1, gen)
