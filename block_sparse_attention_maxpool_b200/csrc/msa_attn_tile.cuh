@@ -63,7 +63,7 @@ constexpr uint32_t kTmemCols = 512;                 // S_A, S_B, O_A, O_B: 128 c
 constexpr uint32_t kOCol = 256;
 constexpr int kPart = 64;                           // keys whose P is handed over at once
 constexpr int kParts = kBlock / kPart;
-constexpr uint32_t kIdescS = umma_idesc_bf16_f32(128, 128, false, false);
+constexpr uint32_t kIdescS = umma_idesc_bf16_f32(128, kPart, false, false);
 constexpr uint32_t kIdescPV = umma_idesc_bf16_f32(128, 128, false, true);
 constexpr float kRescale = 8.f;
 
@@ -81,8 +81,12 @@ struct Rec {
   int32_t block;
   uint32_t mask;      // queries 0-7 (A) and 8-15 (B) that see the block; 0: the tile ends
   int32_t row;        // first cache row
-  int32_t fix;        // some rows may be seen by no query
+  int32_t fix;        // 0: a query sees every row; else some row may be seen by none (kFix*)
+  int32_t lo, hi;     // kFixRange: rows lo .. hi are seen, and those below the sinks' end
+  int32_t pad[2];
 };
+constexpr int32_t kFixRange = 1;   // the queries' windows overlap
+constexpr int32_t kFixExact = 2;   // they may leave gaps: every row is checked against every query
 
 struct Layout {
   static constexpr uint32_t kQOff = 0;                                   // A, B
@@ -120,15 +124,15 @@ struct Bars {
     vland = kempty + kRing;        // [kRing]: the V copy landed
     vready = vland + kRing;        // [kRing]: rows that nobody sees are zero
     vempty = vready + kRing;
-    s_full = vempty + kRing;       // [2]: S of the tile's block is in tensor memory
-    p_full = s_full + 2;           // [2 * 2]: P of the (tile, part) is written (4 softmax warps)
-    pv_done = p_full + 4;          // [2]: the block's P V finished
-    o_empty = pv_done + 2;         // [2]: O was read (4 softmax warps)
+    s_full = vempty + kRing;       // [2 * 2]: S of the (tile, half block) is in tensor memory
+    p_full = s_full + 4;           // [2 * 2]: its P is written (4 softmax warps)
+    pv_done = p_full + 4;          // [2 * 2]: its P V finished
+    o_empty = pv_done + 4;         // [2]: O was read (4 softmax warps)
     mma_done = o_empty + 2;        // [2]: the issuers' last MMAs
     tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   }
 };
-static_assert(2 + 2 * kRecs + 5 * kRing + 4 + 4 * 2 + 1 <= 48, "barrier slots");
+static_assert(2 + 2 * kRecs + 5 * kRing + 3 * 4 + 2 * 2 + 1 <= 48, "barrier slots");
 
 // Task t -> (group, first query).  The last queries (the longest lists of a
 // causal batch) come first, the groups of a tile next to each other, and
@@ -201,7 +205,8 @@ struct Planner {
 
   // Append the records of 32 candidates (one per lane) to the ring, and load
   // their K blocks.
-  __device__ void emit(const CUtensorMap* tm_k, int block, uint32_t mask, bool whole, int s, int g) {
+  __device__ void emit(const CUtensorMap* tm_k, int block, uint32_t mask, bool whole, int pmin, int pmax, int s,
+                       int g) {
     int row = -1;
     if (mask != 0u) {
       row = static_cast<int>(kv_block_row(P.pages, s, g, block, P.G, P.capacity));
@@ -215,7 +220,11 @@ struct Planner {
       in.block = __shfl_sync(0xffffffffu, block, l);
       in.mask = __shfl_sync(0xffffffffu, mask, l);
       in.row = __shfl_sync(0xffffffffu, row, l);
-      in.fix = __shfl_sync(0xffffffffu, whole ? 0 : 1, l);
+      // pmin, pmax: the positions of all of the stream's queries in the tile
+      in.fix = __shfl_sync(0xffffffffu, whole ? 0 : (pmax - pmin < P.window ? kFixRange : kFixExact), l);
+      in.lo = pmin - P.window + 1 - in.block * kBlock;
+      in.hi = pmax - in.block * kBlock;
+      in.pad[0] = in.pad[1] = 0;
       push(in);
       if (ok && lane == 0) {
         const int st = ring % kRing, use = ring / kRing;
@@ -272,10 +281,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.vready[i], 1);
       mbar_init(&B.vempty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&B.p_full[i], 4);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.p_full[i], 4);
       mbar_init(&B.pv_done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&B.o_empty[i], 4);
       mbar_init(&B.mma_done[i], 1);
     }
@@ -317,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           left &= ~seg;
           const bool here = ((seg >> lane) & 1u) != 0u;
           const int pmax = static_cast<int>(__reduce_max_sync(0xffffffffu, here ? static_cast<unsigned>(pos) : 0u));
-          const int a = here ? max(0, pos - P.window + 1) : P.capacity;
-          const int first = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(a))) / kBlock;
+          const int pmin = static_cast<int>(__reduce_min_sync(0xffffffffu, here ? static_cast<unsigned>(pos) : 0x7fffffffu));
+          const int first = max(0, pmin - P.window + 1) / kBlock;
           const int sinks = min((P.n_sink + kBlock - 1) / kBlock, first);
           const int n = sinks + pmax / kBlock - first + 1;
           for (int base = 0; base < n && pl.ok; base += 32) {
@@ -336,10 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 whole |= j1 <= p && (j0 > p - P.window || j1 < P.n_sink);
               }
             }
-            pl.emit(&tm_k, b, i < n ? mask : 0u, whole, s, g);
+            pl.emit(&tm_k, b, i < n ? mask : 0u, whole, pmin, pmax, s, g);
           }
         }
-        if (pl.ok) pl.push(Rec{0, 0u, 0, 0});
+        if (pl.ok) pl.push(Rec{0, 0u, 0, 0, 0, 0, {0, 0}});
       }
       // no copy may still be landing when the CTA exits
       if (lane == 0) {
@@ -348,61 +359,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 2) {
       // --------------------------------- V loader ---------------------------------
+      // A block whose rows are not all seen is finished (its unseen rows set to
+      // zero) after the next block's copy has been issued.
       int r = 0, ring = 0;
       bool ok = true;
+      Rec todo{0, 0u, 0, 0, 0, 0, {0, 0}};
+      int todo_ring = -1;
       for (int k = 0, t = task_at(0); t < n_tasks && ok; t = task_at(++k)) {
         int g, q0, stream;
         bool bad;
         tile_coords(P, t, g, q0);
         const int pos = tile_query(P, q0, lane, stream, bad);
+        auto finish = [&]() {
+          if (todo_ring < 0) return;
+          const int st = todo_ring % kRing;
+          uint8_t* dst = smem + L::kVOff + st * kTile;
+          ok = __all_sync(0xffffffffu, mbar_wait(&B.vland[st], (todo_ring / kRing) & 1));
+#pragma unroll 1
+          for (int i = 0; i < kBlock && ok; i += 32) {
+            const int row = i + lane;
+            const bool seen = todo.fix == kFixRange
+                                  ? row <= todo.hi && (row >= todo.lo || todo.block * kBlock + row < P.n_sink)
+                                  : anyone_sees(P, todo.mask, pos, todo.block * kBlock + row);
+            if (!seen) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                *reinterpret_cast<uint4*>(dst + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(dst + kHalf + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&B.vready[st]);
+          todo_ring = -1;
+        };
         for (;; ++r) {
           Rec in;
-          ok = next_rec(r, in);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, next_rec(r, in));
           if (!ok) break;
+          if (in.mask != 0u) {
+            const int st = ring % kRing, use = ring / kRing;
+            if (lane == 0) {
+              if (use > 0) ok = mbar_wait(&B.vempty[st], (use - 1) & 1);
+              if (ok) {
+                uint8_t* dst = smem + L::kVOff + st * kTile;
+                mbar_arrive_expect_tx(&B.vland[st], kTile);
+                tma_load_2d(dst, &tm_v, 0, in.row, &B.vland[st]);
+                tma_load_2d(dst + kHalf, &tm_v, 64, in.row, &B.vland[st]);
+                if (in.fix == 0) mbar_arrive(&B.vready[st]);
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+          }
+          finish();
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) done_rec(r);
           if (in.mask == 0u) {
-            __syncwarp();
-            if (lane == 0) done_rec(r);
             ++r;
             break;
           }
-          const int st = ring % kRing, use = ring / kRing;
-          uint8_t* dst = smem + L::kVOff + st * kTile;
-          if (lane == 0) {
-            if (use > 0) ok = mbar_wait(&B.vempty[st], (use - 1) & 1);
-            if (ok) {
-              mbar_arrive_expect_tx(&B.vland[st], kTile);
-              tma_load_2d(dst, &tm_v, 0, in.row, &B.vland[st]);
-              tma_load_2d(dst + kHalf, &tm_v, 64, in.row, &B.vland[st]);
-            }
+          if (in.fix != 0) {
+            todo = in;
+            todo_ring = ring;
           }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (ok && in.fix != 0) {
-            ok = mbar_wait(&B.vland[st], use & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            for (int i = 0; i < kBlock && ok; i += 32) {
-              const int row = i + lane;
-              if (!anyone_sees(P, in.mask, pos, in.block * kBlock + row)) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  *reinterpret_cast<uint4*>(dst + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-                  *reinterpret_cast<uint4*>(dst + kHalf + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-              }
-            }
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0 && ok) mbar_arrive(&B.vready[st]);
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
           ++ring;
-          if (lane == 0) done_rec(r);
         }
       }
-      if (lane == 0) {
+      if (lane == 0)
         for (int j = max(0, ring - kRing); j < ring; ++j) mbar_wait(&B.vland[j % kRing], (j / kRing) & 1);
-      }
       __syncwarp();
     } else if (warp == 1) {
       // ------------------- Q loads and the S issuer: S = Q K^T -------------------
@@ -450,21 +477,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&B.kfull[st], (ring / kRing) & 1));
           const uint64_t kd = k_desc + static_cast<uint64_t>(st) * (kTile >> 4);
 #pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
+          for (int i = 0; i < 2 * kParts; ++i) {
+            const int h = i >> 1, x = i & 1;
             const int n = x == 0 ? n0 : n1;
             if (((mask >> (8 * x)) & 0xffu) == 0u || !ok) continue;
-            // the tile's previous P V is done: its S columns are free
-            if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&B.pv_done[x], (n - 1) & 1));
+            // the half's previous P V is done: its S columns are free
+            if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&B.pv_done[2 * x + h], (n - 1) & 1));
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t qd = q_desc + x * (kTile >> 4);
-              const uint32_t d = tmem_base + x * 128;
+              const uint64_t qd = q_desc + x * (kTile >> 4), kh = kd + h * kPart * 8;
+              const uint32_t d = tmem_base + x * 128 + h * kPart;
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk) {
                 const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                umma_f16_ss(d, qd + off, kd + off, idesc, kk != 0);
+                umma_f16_ss(d, qd + off, kh + off, idesc, kk != 0);
               }
-              umma_commit(&B.s_full[x]);
+              umma_commit(&B.s_full[2 * x + h]);
             }
           }
           n0 += (mask & 0xffu) != 0u ? 1 : 0;
@@ -498,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&B.vready[st], use & 1));
 #pragma unroll 1
           for (int i = 0; i < 2 * kParts; ++i) {
-            const int x = i >> 1, h = i & 1;
+            const int h = i >> 1, x = i & 1;
             const int n = x == 0 ? n0 : n1, outs = x == 0 ? outs0 : outs1;
             if (((mask >> (8 * x)) & 0xffu) == 0u || !ok) continue;
             const bool first = ((begun >> x) & 1u) == 0u;
@@ -506,13 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && first && outs > 0) ok = __all_sync(0xffffffffu, mbar_wait(&B.o_empty[x], (outs - 1) & 1));
             tc_fence_after();
             if (elect_one()) {
-              // P: bf16 pairs over the first 64 of S's columns
-              const uint32_t d = tmem_base + kOCol + x * 128, pa = tmem_base + x * 128 + h * (kPart / 2);
+              // P: bf16 pairs over the first half of the half's columns
+              const uint32_t d = tmem_base + kOCol + x * 128, pa = tmem_base + x * 128 + h * kPart;
               const uint64_t vh = vd + h * (kPart / 16) * (2048 >> 4);
 #pragma unroll
               for (int kk = 0; kk < kPart / 16; ++kk)
                 umma_f16_ts(d, pa + kk * 8, vh + kk * (2048 >> 4), kIdescPV, kk == 0 && first ? 0u : 1u);
-              if (h == kParts - 1) umma_commit(&B.pv_done[x]);
+              umma_commit(&B.pv_done[2 * x + h]);
             }
             if (first) {
               if (x == 0) ++outs0;
@@ -575,67 +603,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sink = P.n_sink - j0;
         const bool cut = mine && (hi < kBlock - 1 || (lo > 0 && sink < min(lo, kBlock)));
         const bool any_cut = __any_sync(0xffffffffu, cut);
-        ok = mbar_wait(&B.s_full[x], n & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ++n;
-        tc_fence_after();
-        if (__builtin_expect(any_cut && active, 0)) {
-          // a block that a mask cuts (a few per tile): S is masked in place
-#pragma unroll 1
-          for (int c0 = 0; c0 < kBlock; c0 += 32) {
-            float v[32];
-            tmem_ld32(sbuf + c0, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              v[c] = c0 + c <= hi && (c0 + c >= lo || c0 + c < sink) ? v[c] : -INFINITY;
-            tmem_st32(sbuf + c0, v);
-          }
-          tmem_st_wait();
-        }
-        float neg_m = 0.f;
-        if (active) {
-          // the row maximum, 64 columns at a time: four chains of three-input maxima
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int h = 0; h < kParts; ++h) {
-            float s[kPart];
-            tmem_ld64(sbuf + h * kPart, s);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < kPart; c += 8)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) m4[i] = fmax3(m4[i], s[c + i], s[c + 4 + i]);
-          }
-          const float mb = mine ? fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * f : -INFINITY;
-          const bool raise = mb > m_ref + kRescale;
-          const bool rescale = raise && begun && m_ref != -INFINITY;
-          if (__builtin_expect(__any_sync(0xffffffffu, rescale), 0)) {
-            // S came after the tile's previous P V, so O is at rest
-            const float fo = rescale ? ex2_approx(m_ref - mb) : 1.f;
-            l *= fo;
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              float v[16];
-              tmem_ld16(obuf + c * 16, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] *= fo;
-              tmem_st16(obuf + c * 16, v);
-            }
-          }
-          if (raise) m_ref = mb;
-          neg_m = m_ref == -INFINITY ? 0.f : -m_ref;                     // nothing visible yet
-        }
-        const float2 f2 = make_float2(f, f), nm2 = make_float2(neg_m, neg_m);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int h = 0; h < kParts; ++h) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&B.s_full[2 * x + h], n & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sb = sbuf + h * kPart;
           if (active) {
-            float s[kPart], pk[kPart / 2];
-            tmem_ld64(sbuf + h * kPart, s);
+            if (__builtin_expect(any_cut, 0)) {
+              // a block that a mask cuts (a few per tile): S is masked in place
+#pragma unroll 1
+              for (int c0 = 0; c0 < kPart; c0 += 32) {
+                float v[32];
+                tmem_ld32(sb + c0, v);
+                tmem_ld_wait();
+                const int j = h * kPart + c0;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = j + c <= hi && (j + c >= lo || j + c < sink) ? v[c] : -INFINITY;
+                tmem_st32(sb + c0, v);
+              }
+              tmem_st_wait();
+            }
+            float s[kPart];
+            tmem_ld64(sb, s);
             tmem_ld_wait();
+            // the row maximum: four chains of three-input maxima
+            float m4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = fmax3(s[i], s[4 + i], s[8 + i]);
+#pragma unroll
+            for (int c = 12; c < kPart - 4; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) m4[i] = fmax3(m4[i], s[c + i], s[c + 4 + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], s[kPart - 4 + i]);
+            const float mb = mine ? fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * f : -INFINITY;
+            const bool raise = mb > m_ref + kRescale;
+            const bool rescale = raise && begun && m_ref != -INFINITY;
+            if (__builtin_expect(__any_sync(0xffffffffu, rescale), 0)) {
+              // O is at rest once the P V of the half before has finished
+              const int before = h == 0 ? n - 1 : n;   // count of that half's earlier steps
+              ok = __all_sync(0xffffffffu, mbar_wait(&B.pv_done[2 * x + (h ^ 1)], before & 1));
+              if (!ok) break;
+              tc_fence_after();
+              const float fo = rescale ? ex2_approx(m_ref - mb) : 1.f;
+              l *= fo;
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                float v[16];
+                tmem_ld16(obuf + c * 16, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= fo;
+                tmem_st16(obuf + c * 16, v);
+              }
+            }
+            if (raise) m_ref = mb;
+            const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;       // nothing visible yet
+            const float2 f2 = make_float2(f, f), nm2 = make_float2(neg_m, neg_m);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float pk[kPart / 2];
 #pragma unroll
             for (int i = 0; i < kPart / 2; ++i) {
               const float2 y = ffma2(make_float2(s[2 * i], s[2 * i + 1]), f2, nm2);
@@ -644,27 +671,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc[i & 3] = add_bf16x2_f32(pp, acc[i & 3]);
               pk[i] = __uint_as_float(pp);
             }
-            tmem_st32(sbuf + h * (kPart / 2), pk);
+            tmem_st32(sb, pk);
+            l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
           } else {
             float z[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[i] = 0.f;
-            tmem_st16(sbuf + h * (kPart / 2), z);
-            tmem_st16(sbuf + h * (kPart / 2) + 16, z);
+            tmem_st16(sb, z);
+            tmem_st16(sb + 16, z);
           }
+          begun = true;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&B.p_full[2 * x + h]);
         }
-        begun = true;
-        const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        l += sum;
+        if (!ok) break;
+        ++n;
       }
       if (!ok) break;
       __nv_bfloat16* dst = P.out + (static_cast<size_t>(qi) * (P.G * kHpg) + g * kHpg + (row % kHpg)) * kD;
       if (begun) {
-        ok = mbar_wait(&B.pv_done[x], (n - 1) & 1);
+        ok = mbar_wait(&B.pv_done[2 * x + kParts - 1], (n - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
