@@ -179,6 +179,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       : "memory");
 }
 
+// Columns c0 .. c0 + 63 of a row: those outside lo .. hi and not below `sink`
+// become -inf.
+__device__ __forceinline__ void mask_part(float (&v)[kPart], int c0, int lo, int hi, int sink) {
+  const auto below = [](int n) {                       // bits 0 .. n - 1
+    return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
+  };
+  const unsigned long long seen = below(hi + 1 - c0) & (~below(lo - c0) | below(sink - c0));
+  const uint32_t w[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
+#pragma unroll
+  for (int c = 0; c < kPart; ++c) v[c] = (w[c >> 5] & (1u << (c & 31))) != 0u ? v[c] : -INFINITY;
+}
+
 // Slot j is seen by query position p.
 __device__ __forceinline__ bool sees(const Params& P, int p, int j) {
   return j <= p && (j > p - P.window || j < P.n_sink);
@@ -610,23 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t sb = sbuf + h * kPart;
           if (active) {
-            if (__builtin_expect(any_cut, 0)) {
-              // a block that a mask cuts (a few per tile): S is masked in place
-#pragma unroll 1
-              for (int c0 = 0; c0 < kPart; c0 += 32) {
-                float v[32];
-                tmem_ld32(sb + c0, v);
-                tmem_ld_wait();
-                const int j = h * kPart + c0;
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = j + c <= hi && (j + c >= lo || j + c < sink) ? v[c] : -INFINITY;
-                tmem_st32(sb + c0, v);
-              }
-              tmem_st_wait();
-            }
             float s[kPart];
             tmem_ld64(sb, s);
             tmem_ld_wait();
+            if (__builtin_expect(any_cut, 0)) mask_part(s, h * kPart, lo, hi, sink);
             // the row maximum: four chains of three-input maxima
             float m4[4];
 #pragma unroll
