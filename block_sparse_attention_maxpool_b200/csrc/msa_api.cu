@@ -1141,9 +1141,9 @@ struct ExtAttn {
 
 // CTAs of one pair's cluster: a power of two, as many as keep the grid within
 // two CTAs per SM (what fits at once) and leave every CTA a unit.
-int cluster_ctas(int64_t n_pairs, int64_t units, int sms) {
+int cluster_ctas(int64_t n_pairs, int64_t units, int sms, int per_sm) {
   int k = 1;
-  while (2 * k <= msa::cattn::kMaxCluster && 2 * k <= units && n_pairs * 2 * k <= 2 * static_cast<int64_t>(sms)) k *= 2;
+  while (2 * k <= msa::cattn::kMaxCluster && 2 * k <= units && n_pairs * 2 * k <= per_sm * static_cast<int64_t>(sms)) k *= 2;
   return k;
 }
 
@@ -1153,7 +1153,7 @@ int launch_cluster_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const 
   const auto kernel = msa::cattn::attn_cluster_kernel<kF8, kWin>;
   static std::atomic<uint64_t> smem_done{0};
   static std::atomic<uint64_t> big_done{0};
-  int st = ensure_smem(kernel, msa::cattn::Layout::kBytes, smem_done);
+  int st = ensure_smem(kernel, msa::cattn::Layout<kF8>::kBytes, smem_done);
   if (st != MSA_OK) return st;
   if (k > 8) {
     int dev = 0;
@@ -1168,7 +1168,7 @@ int launch_cluster_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_pairs * k));
   cfg.blockDim = dim3(msa::cattn::kThreads);
-  cfg.dynamicSmemBytes = msa::cattn::Layout::kBytes;
+  cfg.dynamicSmemBytes = msa::cattn::Layout<kF8>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1317,7 +1317,8 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   const int64_t units = win ? std::min<int64_t>(sh->capacity / unit_rows, (P.window + unit_rows - 1) / unit_rows + 1 +
                                                                               (P.n_sink + unit_rows - 1) / unit_rows)
                             : msa::cattn::kTopK * (128 / unit_rows);
-  const int k = cluster_ctas(n_pairs, units, sms);
+  const int k = cluster_ctas(n_pairs, units, sms,
+                             a.f8 ? msa::cattn::Unit<true>::kCtas : msa::cattn::Unit<false>::kCtas);
   if (win)
     return a.f8 ? launch_cluster_attn<true, true>(tm_k, tm_v, P, n_pairs, k, s)
                 : launch_cluster_attn<false, true>(tm_k, tm_v, P, n_pairs, k, s);

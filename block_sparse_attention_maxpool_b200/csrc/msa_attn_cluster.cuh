@@ -21,13 +21,18 @@
 // global memory between CTAs: no workspace, no flags, no order of arrival,
 // the same result every time.
 //
+// O and the sum of the p have references (the exponent that counts as 2^0)
+// that are raised only when a unit passes them by a few powers of two, so O
+// is hardly ever rescaled.
+//
 // e4m3 rows: K and V values are converted exactly to fp16, and the MMAs take
 // fp16.  q keeps its 8 significant bits in fp16 after a power-of-two scaling
 // of each head's row to a largest magnitude in [2^14, 2^15) (elements more
 // than 2^29 below it lose bits); the block's K scale, the head's scaling and
-// c are one float32 factor of the score.  p is held as 2^14 p (nearest fp16,
-// 11 bits; it stays normal down to p = 2^-28), and each unit's P V is added
-// to O with its V scale in float32.  bf16 rows: p is rounded to bf16, the
+// c are one float32 factor of the score.  The V scale joins the exponent: p vs
+// is what O adds up, rounded to fp16 (11 bits, normal down to 2^-24 of the
+// reference) with a reference of its own, which follows the largest p vs; the
+// p are summed in float32, unrounded.  bf16 rows: p is rounded to bf16, the
 // row sum adds the rounded values.
 //
 // ldmatrix moves 16-bit pairs, so on e4m3 tiles it hands a thread four
@@ -54,7 +59,6 @@ constexpr int kHpg = 16;
 constexpr int kTopK = 16;
 constexpr int kWarps = 4;                        // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;      // and the producer warp
-constexpr int kStages = 3;
 constexpr uint32_t kStageBytes = 32768;          // K and V of one unit
 constexpr uint32_t kHalfStage = kStageBytes / 2;
 constexpr int kMaxCluster = 16;
@@ -64,6 +68,8 @@ template <bool kF8>
 struct Unit {
   static constexpr int kRows = kF8 ? 128 : 64;
   static constexpr int kWarpRows = kRows / kWarps;
+  static constexpr int kStages = 3;
+  static constexpr int kCtas = 2;     // CTAs per SM
 };
 
 // What the producer tells the consumers about the unit in a stage.
@@ -75,18 +81,21 @@ struct UnitInfo {
   int32_t pad[2];
 };
 
+template <bool kF8>
 struct Layout {
+  static constexpr int kStages = Unit<kF8>::kStages;
   static constexpr uint32_t kMergeOff = 0;                                       // [4][16][kOStride], over the ring
-  static constexpr uint32_t kMergeMlOff = kWarps * kHpg * kOStride * 4;          // [4][16][2], over the ring
+  static constexpr uint32_t kMergeMlOff = kWarps * kHpg * kOStride * 4;          // [4][16][4], over the ring
   static constexpr uint32_t kOutOff = kStages * kStageBytes;                     // the CTA's merged O [16][128]
-  static constexpr uint32_t kMlOff = kOutOff + kHpg * kD * 4;                    // and its m, l [16][2]
-  static constexpr uint32_t kInfoOff = kMlOff + kHpg * 2 * 4;
+  static constexpr uint32_t kMlOff = kOutOff + kHpg * kD * 4;                    // and its references, sum [16][4]
+  static constexpr uint32_t kInfoOff = kMlOff + kHpg * 4 * 4;
   static constexpr uint32_t kBarOff = kInfoOff + kStages * sizeof(UnitInfo);
   static constexpr uint32_t kEnd = kBarOff + 2 * kStages * 8;
   static constexpr size_t kBytes = kEnd + 1024;
 };
-static_assert(Layout::kMergeMlOff + kWarps * kHpg * 2 * 4 <= kStages * kStageBytes, "merge buffer fits the ring");
-static_assert(2 * (Layout::kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(Layout<true>::kMergeMlOff + kWarps * kHpg * 4 * 4 <= 2 * kStageBytes, "merge buffer fits the ring");
+static_assert(2 * (Layout<true>::kBytes + 1024) <= 228 * 1024 && 2 * (Layout<false>::kBytes + 1024) <= 228 * 1024,
+              "CTAs per SM");
 
 struct Params {
   const __nv_bfloat16* q;     // [n_q][16 G][128]
@@ -143,10 +152,12 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
   return d;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+
+__device__ __forceinline__ void ld_cluster4(uint32_t addr, float (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr)
+               : "memory");
 }
 
 // The units of query position p: n of them; unit i covers the slots from
@@ -172,12 +183,19 @@ struct Units {
 };
 
 template <bool kF8, bool kWin>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Unit<kF8>::kCtas)
     attn_cluster_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const Params P, const int cluster) {
+  using Layout = cattn::Layout<kF8>;
+  constexpr int kStages = Unit<kF8>::kStages;
   constexpr int kRows = Unit<kF8>::kRows;
   constexpr int kWarpRows = Unit<kF8>::kWarpRows;
   constexpr int kSub = kWarpRows / 16;                 // 16-row steps of a warp's share of a unit
+  // O's reference m_o is raised only when a unit passes it by more than
+  // kRaise (log2 units); p is held as 2^kLift p, at most 2^14 in fp16
+  constexpr float kRaise = kF8 ? 4.f : 8.f;
+  constexpr float kLift = kF8 ? 10.f : 0.f;
+  constexpr float kRaiseSum = 32.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Layout::kBarOff);
@@ -336,12 +354,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-    // p is held as 2^kLift p
-    constexpr float kLift = kF8 ? 14.f : 0.f;
     float o[16][4];
 #pragma unroll
     for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    float m_o[2] = {-INFINITY, -INFINITY}, m_l[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     const int wr = warp * kWarpRows;
     bool ok = true;
     for (int k = 0; k < u1 - u0; ++k) {
@@ -360,17 +376,18 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int t = 0; t < 2 * kSub; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
         if (kF8) {
-          // one x4: 8 rows x 64 dims, i.e. four k-steps of one n tile
+          // one x4: 8 rows x 64 dims, i.e. four k-steps of one n tile; the n
+          // tiles take turns, so that successive MMAs do not wait for each other
 #pragma unroll
-          for (int t = 0; t < 2 * kSub; ++t) {
+          for (int half = 0; half < 2; ++half) {
+            uint32_t b[2 * kSub][4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t b[4];
-              ldmatrix_x4(b, kbase + swz128(wr + t * 8 + l7, half * 4 + mi));
+            for (int t = 0; t < 2 * kSub; ++t) ldmatrix_x4(b[t], kbase + swz128(wr + t * 8 + l7, half * 4 + mi));
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_f16_16816(sc[t], qa[half * 4 + i], e4m3_to_f16x2(b[i]), e4m3_to_f16x2(b[i] >> 16));
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int t = 0; t < 2 * kSub; ++t)
+                mma_f16_16816(sc[t], qa[half * 4 + i], e4m3_to_f16x2(b[t][i]), e4m3_to_f16x2(b[t][i] >> 16));
           }
         } else {
 #pragma unroll
@@ -386,81 +403,40 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int t = 0; t < 2 * kSub; ++t) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = wr + t * 8 + tq * 2 + (e & 1);
-            float x = sc[t][e] * (e < 2 ? f0 : f1);
-            if (cut) x = r <= in.hi && (r >= in.lo || r < in.sink) ? x : -INFINITY;
-            sc[t][e] = x;
-            mx[e >> 1] = fmaxf(mx[e >> 1], x);
+          for (int e = 0; e < 4; ++e) sc[t][e] *= e < 2 ? f0 : f1;
+        }
+        if (cut) {
+#pragma unroll
+          for (int t = 0; t < 2 * kSub; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = wr + t * 8 + tq * 2 + (e & 1);
+              if (r > in.hi || (r < in.lo && r >= in.sink)) sc[t][e] = -INFINITY;
+            }
           }
         }
-        float alpha[2], m_use[2];
+#pragma unroll
+        for (int t = 0; t < 2 * kSub; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], sc[t][e]);
+        // log2 of the V scale: a unit's rows weigh p * vs in O
+        const float lvs = kF8 ? __log2f(fabsf(in.vs)) : 0.f;
+        bool up[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
           mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-          const float m_new = fmaxf(m_run[h], mx[h]);
-          m_use[h] = m_new == -INFINITY ? 0.f : m_new;
-          alpha[h] = ex2(m_run[h] - m_use[h]);
-          m_run[h] = m_new;
-          m_use[h] -= kLift;
+          up[h] = mx[h] + lvs > m_o[h] + kRaise;
         }
-        uint32_t pa[kSub][4];
-        float rs[2] = {0.f, 0.f};
-#pragma unroll
-        for (int t = 0; t < 2 * kSub; ++t) {
+        if (__any_sync(0xffffffffu, up[0] || up[1])) {
+          float alpha[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float x = ex2(sc[t][2 * h] - m_use[h]), y = ex2(sc[t][2 * h + 1] - m_use[h]);
-            const uint32_t w = kF8 ? pack_f16(x, y) : pack_bf16(x, y);
-            if (kF8) {
-              const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&w));
-              rs[h] += z.x + z.y;
-            } else {
-              rs[h] += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
-            }
-            pa[t >> 1][(t & 1) * 2 + h] = w;
+            const float m_new = up[h] ? mx[h] + lvs : m_o[h];
+            alpha[h] = m_o[h] == m_new ? 1.f : ex2(m_o[h] - m_new);      // 0 the first time
+            m_o[h] = m_new;
+            if (!kF8) l_run[h] *= alpha[h];
           }
-        }
-        l_run[0] = l_run[0] * alpha[0] + rs[0];
-        l_run[1] = l_run[1] * alpha[1] + rs[1];
-        // V rows that the masks cut off count as zeros
-        uint32_t keep[kSub][2];
-#pragma unroll
-        for (int u = 0; u < kSub; ++u) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = wr + u * 16 + i * 8 + tq * 2;
-            const bool a = r <= in.hi && (r >= in.lo || r < in.sink);
-            const bool b = r + 1 <= in.hi && (r + 1 >= in.lo || r + 1 < in.sink);
-            keep[u][i] = (a ? 0x0000ffffu : 0u) | (b ? 0xffff0000u : 0u);
-          }
-        }
-        if (kF8) {
-          // 16 dims at a time: tile n the even ones, n + 1 the odd ones
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t v[4];                             // rows 0-7, 8-15, 16-23, 24-31 of the warp's 32
-            ldmatrix_x4_trans(v, vbase + swz128(wr + mi * 8 + l7, c));
-#pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-              uint32_t x = v[2 * u], y = v[2 * u + 1];
-              if (cut) {
-                x &= keep[u][0];
-                y &= keep[u][1];
-              }
-              const uint32_t x2 = __byte_perm(x, 0u, 0x3120), y2 = __byte_perm(y, 0u, 0x3120);
-              mma_f16_16816(d0, pa[u], e4m3_to_f16x2(x2), e4m3_to_f16x2(y2));
-              mma_f16_16816(d1, pa[u], e4m3_to_f16x2(x2 >> 16), e4m3_to_f16x2(y2 >> 16));
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[2 * c][e] = o[2 * c][e] * alpha[e >> 1] + d0[e] * in.vs;
-              o[2 * c + 1][e] = o[2 * c + 1][e] * alpha[e >> 1] + d1[e] * in.vs;
-            }
-          }
-        } else {
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
             o[n][0] *= alpha[0];
@@ -468,6 +444,75 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[n][2] *= alpha[1];
             o[n][3] *= alpha[1];
           }
+        }
+        // e4m3: the sum of the p has a reference of its own, raised rarely
+        // (float32 has room)
+        if (kF8 && __any_sync(0xffffffffu, mx[0] > m_l[0] + kRaiseSum || mx[1] > m_l[1] + kRaiseSum)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (mx[h] > m_l[h]) {
+              l_run[h] *= ex2(m_l[h] - mx[h]);
+              m_l[h] = mx[h];
+            }
+          }
+        }
+        uint32_t pa[kSub][4];
+        float rs[2] = {0.f, 0.f};
+        // (m_o still -inf: everything masked, or a V scale of zero)
+        const float off[2] = {m_o[0] == -INFINITY ? -INFINITY : lvs - m_o[0] + kLift,
+                              m_o[1] == -INFINITY ? -INFINITY : lvs - m_o[1] + kLift};
+        const float off_l[2] = {m_l[0] == -INFINITY ? 0.f : -m_l[0], m_l[1] == -INFINITY ? 0.f : -m_l[1]};
+        const uint32_t sign = kF8 && in.vs < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int t = 0; t < 2 * kSub; ++t) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float x = ex2(sc[t][2 * h] + off[h]), y = ex2(sc[t][2 * h + 1] + off[h]);
+            uint32_t w;
+            if (kF8) {
+              w = pack_f16(x, y) ^ sign;
+              rs[h] += ex2(sc[t][2 * h] + off_l[h]) + ex2(sc[t][2 * h + 1] + off_l[h]);
+            } else {
+              w = pack_bf16(x, y);
+              rs[h] += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
+            }
+            pa[t >> 1][(t & 1) * 2 + h] = w;
+          }
+        }
+        l_run[0] += rs[0];
+        l_run[1] += rs[1];
+        // V rows that the masks cut off count as zeros
+        uint32_t keep[kSub][2];
+        if (cut) {
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = wr + u * 16 + i * 8 + tq * 2;
+              const bool a = r <= in.hi && (r >= in.lo || r < in.sink);
+              const bool b = r + 1 <= in.hi && (r + 1 >= in.lo || r + 1 < in.sink);
+              keep[u][i] = (a ? 0x0000ffffu : 0u) | (b ? 0xffff0000u : 0u);
+            }
+          }
+        }
+        if (kF8) {
+          // 16 dims at a time: tile n the even ones, n + 1 the odd ones
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[4];                             // rows 0-7, 8-15, 16-23, 24-31 of the warp's 32
+            ldmatrix_x4_trans(v, vbase + swz128(wr + mi * 8 + l7, c));
+            if (cut) {
+#pragma unroll
+              for (int u = 0; u < 2 * kSub; ++u) v[u] &= keep[u >> 1][u & 1];
+            }
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+              const uint32_t x2 = __byte_perm(v[2 * u], 0u, 0x3120), y2 = __byte_perm(v[2 * u + 1], 0u, 0x3120);
+              mma_f16_16816(o[2 * c], pa[u], e4m3_to_f16x2(x2), e4m3_to_f16x2(y2));
+              mma_f16_16816(o[2 * c + 1], pa[u], e4m3_to_f16x2(x2 >> 16), e4m3_to_f16x2(y2 >> 16));
+            }
+          }
+        } else {
 #pragma unroll
           for (int jn = 0; jn < 8; ++jn) {
             uint32_t v[4];
@@ -494,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     named_barrier_sync(1, kWarps * 32);
     float* so = reinterpret_cast<float*>(smem + Layout::kMergeOff) + warp * kHpg * kOStride;
-    float* sml = reinterpret_cast<float*>(smem + Layout::kMergeMlOff) + warp * kHpg * 2;
+    float* sml = reinterpret_cast<float*>(smem + Layout::kMergeMlOff) + warp * kHpg * 4;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       if (kF8) {
@@ -512,10 +557,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (tq == 0) {
-      sml[gr * 2] = m_run[0];
-      sml[gr * 2 + 1] = l_run[0];
-      sml[(gr + 8) * 2] = m_run[1];
-      sml[(gr + 8) * 2 + 1] = l_run[1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float4*>(sml + (gr + 8 * h) * 4) = make_float4(m_o[h], kF8 ? m_l[h] : m_o[h], l_run[h], 0.f);
     }
     named_barrier_sync(1, kWarps * 32);
     // the CTA's state: thread (head, 16 dims)
@@ -523,17 +567,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int head = tid >> 3, dd = (tid & 7) * 16;
     const float* all = reinterpret_cast<const float*>(smem + Layout::kMergeOff);
     const float* allml = reinterpret_cast<const float*>(smem + Layout::kMergeMlOff);
-    float M = -INFINITY, L = 0.f;
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, allml[(w * kHpg + head) * 2]);
-    const float Mu = M == -INFINITY ? 0.f : M;
+    float Mo = -INFINITY, Ml = -INFINITY, L = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(allml[(w * kHpg + head) * 2] - Mu);
-      L += allml[(w * kHpg + head) * 2 + 1] * f;
+      Mo = fmaxf(Mo, allml[(w * kHpg + head) * 4]);
+      Ml = fmaxf(Ml, allml[(w * kHpg + head) * 4 + 1]);
+    }
+    const float uo = Mo == -INFINITY ? 0.f : Mo, ul = Ml == -INFINITY ? 0.f : Ml;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 ml = *reinterpret_cast<const float4*>(allml + (w * kHpg + head) * 4);
+      const float f = ex2(ml.x - uo);
+      L += ml.z * ex2(ml.y - ul);
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const float4 v = *reinterpret_cast<const float4*>(all + (w * kHpg + head) * kOStride + dd + i);
@@ -544,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (cluster == 1) {
-      const float inv = L != 0.f ? 1.f / L : 0.f;
+      const float inv = L != 0.f ? ex2(uo - ul - kLift) / L : 0.f;
       uint32_t w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = pack_bf16(acc[2 * i] * inv, acc[2 * i + 1] * inv);
@@ -557,9 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<float4*>(mine + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
       if ((tid & 7) == 0) {
-        float* ml = reinterpret_cast<float*>(smem + Layout::kMlOff) + head * 2;
-        ml[0] = M;
-        ml[1] = L;
+        *reinterpret_cast<float4*>(smem + Layout::kMlOff + head * 16) = make_float4(Mo, Ml, L, 0.f);
       }
     }
   }
@@ -567,31 +613,37 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncwarp();
   cluster_sync();                                      // every CTA's state is in its shared memory
   if (warp < kWarps) {
-    // this CTA's slice of the output: 2048 / cluster elements, 16 / cluster per thread
-    const int per = 16 / cluster;
-    const int e0 = rank * (kHpg * kD / cluster) + static_cast<int>(threadIdx.x) * per;
-    const int head = e0 / kD;
-    const uint32_t obase = smem_addr(smem + Layout::kOutOff) + e0 * 4;
-    const uint32_t mbase = smem_addr(smem + Layout::kMlOff) + head * 8;
-    float M = -INFINITY;
-    for (int c = 0; c < cluster; ++c) M = fmaxf(M, ld_cluster(map_rank(mbase, c)));
-    const float Mu = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[8];
+    // rank r writes heads r, r + cluster, ...: a quarter of a warp's lanes per
+    // 32 dims, four dims a lane
+    for (int head = rank + warp * cluster; head < kHpg; head += kWarps * cluster) {
+      const uint32_t obase = smem_addr(smem + Layout::kOutOff) + (head * kD + lane * 4) * 4;
+      // lane c < cluster holds rank c's references and sum
+      float ml[4] = {-INFINITY, -INFINITY, 0.f, 0.f};
+      if (lane < cluster) ld_cluster4(map_rank(smem_addr(smem + Layout::kMlOff) + head * 16, lane), ml);
+      float Mo = ml[0], Ml = ml[1];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    for (int c = 0; c < cluster; ++c) {
-      const uint32_t ma = map_rank(mbase, c), oa = map_rank(obase, c);
-      const float f = ex2(ld_cluster(ma) - Mu);
-      L += ld_cluster(ma + 4) * f;
+      for (int o = 16; o > 0; o >>= 1) {
+        Mo = fmaxf(Mo, __shfl_xor_sync(0xffffffffu, Mo, o));
+        Ml = fmaxf(Ml, __shfl_xor_sync(0xffffffffu, Ml, o));
+      }
+      const float uo = Mo == -INFINITY ? 0.f : Mo, ul = Ml == -INFINITY ? 0.f : Ml;
+      const float fc = ex2(ml[0] - uo);
+      float L = lane < cluster ? ml[2] * ex2(ml[1] - ul) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < per) acc[i] += ld_cluster(oa + 4 * i) * f;
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int c = 0; c < cluster; ++c) {
+        float v[4];
+        ld_cluster4(map_rank(obase, c), v);
+        const float f = __shfl_sync(0xffffffffu, fc, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += v[i] * f;
+      }
+      const float inv = L != 0.f ? ex2(uo - ul - kLift) / L : 0.f;
+      *reinterpret_cast<uint2*>(P.out + (static_cast<size_t>(pair) * kHpg + head) * kD + lane * 4) =
+          make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
     }
-    const float inv = L != 0.f ? 1.f / L : 0.f;
-    __nv_bfloat16* dst = P.out + static_cast<size_t>(pair) * kHpg * kD + e0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < per) dst[i] = __float2bfloat16_rn(acc[i] * inv);
   }
   __syncwarp();
   cluster_sync();                                      // no CTA leaves while another reads its shared memory

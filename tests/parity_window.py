@@ -21,16 +21,26 @@ from oracle import cache_ops as C
 
 U = 2.0 ** -24
 P_BF16, P_FP16 = 2.0 ** -8, 2.0 ** -11
+
+
+def norm_of(f8, mode, n, S):
+    """norm_round of a call: see check_attention (prefill calls with 64 queries per stream expand an 8-bit cache)."""
+    return P_FP16 if f8 and not (mode == "prefill" and n >= 64 * min(S, n)) else 0.0
+
+
 POISON = float("nan")
 
 
-def check_attention(got, want, spread, reach, p_round, kv_round=0.0):
+def check_attention(got, want, spread, reach, p_round, kv_round=0.0, norm_round=0.0):
     """kv_round: rounding of the K and V values themselves (2^-8 where an 8-bit cache with scales that are no powers
     of two is expanded to bf16): a score moves by kv_round times ``reach`` at most, out by kv_round sum_j w_j |v_j|,
-    which is at most spread + |out|."""
+    which is at most spread + |out|.
+    norm_round: where the sum of the p is not that of the rounded p (single queries over an 8-bit cache: p in fp16, 2^-11),
+    out = sum_j w_j (1 + d_j) v_j, off by at most |d| sum_j w_j |v_j| <= |d| (spread + |out|), of which p_round covers
+    the first part."""
     d = p_round + 2 * (138 * U + kv_round) * reach + 2.0 ** -18
     tol = d / (1 - d).clamp_min(0.5) * spread + 2.0 ** -8 * want.abs() * (1 + 2.0 ** -7) + 1e-30
-    tol = tol + kv_round * (spread + want.abs())
+    tol = tol + (kv_round + norm_round) * (spread + want.abs())
     g = got.double().cpu()
     assert bool(g.isfinite().all()), "not finite"
     err = (g - want).abs()

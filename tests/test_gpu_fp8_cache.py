@@ -226,7 +226,7 @@ def test_selected_attention(mode, S, G, cap, n, paged, pow2):
     assert got is out
     PW.device_error()
     kv_round = 2.0 ** -8 if mode == "prefill" and not pow2 and n >= 64 * S else 0.0
-    print(f"\n[fp8 {mode}] of its bound: {PW.check_attention(got, want, spread, reach, PW.P_BF16, kv_round):.2f}")
+    print(f"\n[fp8 {mode}] of its bound: {PW.check_attention(got, want, spread, reach, PW.P_BF16, kv_round, PW.norm_of(True, mode, n, S)):.2f}")
 
 
 @pytest.mark.parametrize("mode", ["decode", "prefill"])
@@ -283,7 +283,7 @@ def test_decode_step_on_8bit_caches(prefill):
     q, _ = msa.msa_rope_append(shape, rope, q=new["q"], q_pos=new["q_pos"])
     k, v = (C.fp8_values(c[x + "_cache"].cpu(), c[x + "_scale"].cpu()) for x in "kv")
     want, spread, reach = C.selected_attention(q.cpu(), k, v, sel.cpu(), stream, pos, 128 ** -0.5)
-    PW.check_attention(out, want, spread, reach, PW.P_BF16)
+    PW.check_attention(out, want, spread, reach, PW.P_BF16, 0.0, PW.norm_of(True, "prefill" if prefill else "decode", n, S))
     assert bool((n_sel >= 1).all())
     graph = msa.DecodeGraph(shape, fresh(), new, prefill=prefill, rope=rope)
     assert torch.equal(graph.replay(), out)

@@ -98,7 +98,7 @@ def test_against_oracle(mode, f8, paged, case):
     want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, window, sink, 128 ** -0.5)
     got = run(mode, shape, q, kv, stream, pos, window, sink, table, n_pages)
     PW.device_error()
-    PW.check_attention(got, want, spread, reach, PW.P_BF16)
+    PW.check_attention(got, want, spread, reach, PW.P_BF16, 0.0, PW.norm_of(f8, mode, len(at), S))
 
 
 @pytest.mark.parametrize("f8", [False, True])
@@ -115,7 +115,7 @@ def test_long_windows_split_over_ctas(f8, S, G, cap, window, sink):
     got = run("decode", shape, q, kv, stream, pos, window, sink)
     again = run("decode", shape, q, kv, stream, pos, window, sink)
     PW.device_error()
-    PW.check_attention(got, want, spread, reach, PW.P_BF16)
+    PW.check_attention(got, want, spread, reach, PW.P_BF16, 0.0, PW.norm_of(f8, "decode", S, S))
     assert torch.equal(got, again)
 
 
@@ -133,7 +133,7 @@ def test_steep_scores(mode, f8):
     for scale in (128 ** -0.5, -0.05, 0.0):
         want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, 500, 10, scale)
         got = run(mode, shape, q, kv, stream, pos, 500, 10, scale=scale)
-        PW.check_attention(got, want, spread, reach, PW.P_BF16)
+        PW.check_attention(got, want, spread, reach, PW.P_BF16, 0.0, PW.norm_of(f8, mode, n, 1))
     PW.device_error()
 
 
@@ -166,7 +166,7 @@ def test_invalid_queries_and_unmapped_pages(mode, f8):
     attend(mode, shape, q.cuda(), args[0][0], args[1][0], stream.cuda(), pos.cuda(), window, sink, out=out,
            pages=msa.Pages(bad.cuda(), n_pages), k_scale=args[0][1], v_scale=args[1][1])
     PW.device_error(0x1 | 0x10)
-    PW.check_attention(out, want, spread, reach, PW.P_BF16)
+    PW.check_attention(out, want, spread, reach, PW.P_BF16, 0.0, PW.norm_of(f8, mode, n, S))
     assert not bool(out[(stream < 0) | (stream > 1) | (pos < 0) | (pos >= cap)].any())
 
 
@@ -209,7 +209,7 @@ def test_window_steps_in_a_row(prefill, f8):
         q, _ = msa.msa_rope_append(shape, rope, q=new["q"], q_pos=new["q_pos"])
         k, v = logical()
         want = C.window_attention(q.cpu(), k, v, new["q_stream"].cpu(), new["q_pos"].cpu(), 150, 20, 128 ** -0.5)
-        PW.check_attention(out, *want, PW.P_BF16)
+        PW.check_attention(out, *want, PW.P_BF16, 0.0, PW.norm_of(f8, "prefill" if prefill else "decode", S * n_new, S))
     for _ in range(3):
         new = inputs()
         side.wait_stream(torch.cuda.current_stream())
@@ -270,4 +270,29 @@ def test_large_offsets():
     for mode in ("decode", "prefill"):
         got = attend(mode, shape, q.cuda(), k, v, stream.cuda(), pos.cuda(), 300, 4, pages=msa.Pages(ids.cuda(), n_pages))
         PW.check_attention(got, *want, PW.P_BF16)
+    PW.device_error()
+
+
+@pytest.mark.parametrize("spread_v", [False, True])
+def test_far_apart_scales(spread_v):
+    """8-bit blocks whose K and V scales differ by up to 2^60 (a block of zeros, a block with a zero scale among them),
+    so that the block with the largest values and the one with the largest weights are different ones."""
+    gen = torch.Generator().manual_seed(15)
+    shape = msa.Shape(1, 1280, 16, 1)
+    S = [1.0, 2.0 ** -40, 2.0 ** 20, 0.0, 2.0 ** -20, 2.0 ** -100, 3.0, 2.0 ** 10, 0.7, 1.3]
+    kv = []
+    for i in range(2):
+        q8, _ = PW.quantise(torch.randn((1, 1, 1280, 128), generator=gen))
+        q8 = q8.view(torch.uint8).clone()
+        q8[:, :, 640:768] = 0                                   # block 5: zeros
+        q8 = q8.view(F8)
+        sc = torch.tensor(S if i == 1 or not spread_v else [1.0 / 448] * 10).view(1, 1, 10)
+        sc = sc / (448 if i else 2.0 ** 24)                     # scores up to a few hundred where K has the scales
+        kv.append((q8, sc, C.fp8_values(q8, sc)))
+    q = torch.randn((4, 16, 128), generator=gen).bfloat16()
+    stream, pos = torch.zeros(4, dtype=torch.int32), torch.tensor([1279, 700, 500, 130], dtype=torch.int32)
+    for window in (2000, 300, 100):
+        want, spread, reach = C.window_attention(q, kv[0][2], kv[1][2], stream, pos, window, 4, 128 ** -0.5)
+        got = run("decode", shape, q, kv, stream, pos, window, 4, poison=False)
+        PW.check_attention(got, want, spread, reach, PW.P_BF16, 0.0, PW.P_FP16)
     PW.device_error()
