@@ -73,8 +73,12 @@ class Shape:
         return self.capacity // self.block
 
     def c(self) -> CShape:
-        return CShape(self.n_streams, self.capacity, self.n_q_heads, self.n_kv_heads,
-                      self.head_dim, self.idx_dim, self.block, self.top_k)
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = CShape(self.n_streams, self.capacity, self.n_q_heads, self.n_kv_heads,
+                       self.head_dim, self.idx_dim, self.block, self.top_k)
+            object.__setattr__(self, "_c", c)          # the library only reads it
+        return c
 
 
 class CPages(ctypes.Structure):
@@ -588,38 +592,39 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
 
 
 # ---- rotating appends, 8-bit caches, window attention ---------------------------
-def _dptr(t: torch.Tensor, dtype, shape, name: str, dev) -> int:
-    """_ptr of a tensor that has to be on ``dev``, the call's device."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+def _dptr(t: torch.Tensor, dtype, shape, name: str, dev: int) -> int:
+    """_ptr of a tensor that has to be on CUDA device ``dev``, the call's device."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     p = _ptr(t, dtype, shape, name)
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     return p
 
 
-def _device_of(t: torch.Tensor, name: str):
+def _device_of(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def _on(dev, stream):
-    """The raw stream a call on ``dev`` launches on."""
+def _on(dev: int, stream) -> int:
+    """The raw stream a call on device ``dev`` launches on."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream)
 
 
-def _launch(fn: str, dev, args) -> None:
+def _launch(fn: str, dev: int, args) -> None:
     """Call ``fn`` with ``dev`` as the current device (the library launches on it)."""
-    f = getattr(library(), fn)
-    if dev.index == torch.cuda.current_device():
+    f = getattr(_lib or library(), fn)
+    if torch._C._cuda_getDevice() == dev:
         status = f(*args)
     else:
         with torch.cuda.device(dev):
             status = f(*args)
-    _check(fn, status)
+    if status != 0:
+        raise MsaError(fn, status)
 
 
 def _pages_arg(shape: Shape, pages: Pages | None, dev):
@@ -677,9 +682,9 @@ def msa_rope_append(shape: Shape, rope: Rope, k_cache=None, v_cache=None, k_new=
     if not any(given) and idx_k_cache is None:
         nt = 0
     if q is not None and q_out is None:
-        q_out = torch.empty((nq, shape.n_q_heads, D), dtype=torch.bfloat16, device=dev)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if idx_q is not None and idx_q_out is None:
-        idx_q_out = torch.empty((nq, G, Di), dtype=torch.float32, device=dev)
+        idx_q_out = torch.empty_like(idx_q, memory_format=torch.contiguous_format)
     k = [0, 0, 0, 0, 0]
     if any(given):
         cs, ns = _cache_shape(shape, pages, D), (nt, G, D)
@@ -718,15 +723,18 @@ def msa_kv_append_fp8(shape: Shape, k_cache, v_cache, k_scale, v_scale, k_new, v
     dev = _device_of(tok_pos, "tok_pos")
     cs, ss = _cache_shape(shape, pages, shape.head_dim), _scale_shape(shape, pages)
     ns = (n, shape.n_kv_heads, shape.head_dim)
+    need = 0
     if workspace is None:
-        workspace = torch.empty((msa_kv_append_fp8_workspace_bytes(shape, n),), dtype=torch.uint8, device=dev)
+        need = msa_kv_append_fp8_workspace_bytes(shape, n)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need > 0 else None
     _launch("msa_kv_append_fp8", dev, (
         shape.c(), _pages_arg(shape, pages, dev), None if rope is None else rope.c(dev),
         _dptr(k_cache, torch.float8_e4m3fn, cs, "k_cache", dev), _dptr(v_cache, torch.float8_e4m3fn, cs, "v_cache", dev),
         _dptr(k_scale, torch.float32, ss, "k_scale", dev), _dptr(v_scale, torch.float32, ss, "v_scale", dev),
         _dptr(k_new, torch.bfloat16, ns, "k_new", dev), _dptr(v_new, torch.bfloat16, ns, "v_new", dev),
         _dptr(tok_stream, torch.int32, (n,), "tok_stream", dev), _dptr(tok_pos, torch.int32, (n,), "tok_pos", dev), n,
-        _dptr(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel(), _on(dev, stream)))
+        0 if workspace is None else _dptr(workspace, torch.uint8, workspace.shape, "workspace", dev),
+        0 if workspace is None else workspace.numel(), _on(dev, stream)))
 
 
 def msa_attn_workspace_bytes(shape: Shape, n_q: int, mode: int, fp8: bool = False) -> int:
@@ -742,8 +750,9 @@ def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_
     n = _n(q_pos, "q_pos")
     dev = _device_of(q, "q")
     qs = (n, shape.n_q_heads, shape.head_dim)
+    qp = _dptr(q, torch.bfloat16, qs, "q", dev)
     if out is None:
-        out = torch.empty(qs, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q)
     cs = _cache_shape(shape, pages, shape.head_dim)
     if k_cache.dtype is torch.float8_e4m3fn:
         if k_scale is None or v_scale is None:
@@ -766,7 +775,7 @@ def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_
         wp, wb = _dptr(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel()
     if softmax_scale is None:
         softmax_scale = shape.head_dim ** -0.5
-    _launch(fn, dev, (shape.c(), _pages_arg(shape, pages, dev), _dptr(q, torch.bfloat16, qs, "q", dev), *kv, *extra,
+    _launch(fn, dev, (shape.c(), _pages_arg(shape, pages, dev), qp, *kv, *extra,
                       _dptr(q_stream, torch.int32, (n,), "q_stream", dev), _dptr(q_pos, torch.int32, (n,), "q_pos", dev),
                       n, *tail, softmax_scale, _dptr(out, torch.bfloat16, qs, "out", dev), wp, wb, _on(dev, stream)))
     return out

@@ -1398,7 +1398,7 @@ int msa_rope_append(const msa_shape* shape, const msa_pages* pages, const msa_ro
 
 size_t msa_kv_append_fp8_workspace_bytes(const msa_shape* shape, int32_t n_tok) {
   if (check_shape(shape) != MSA_OK || n_tok < 0) return static_cast<size_t>(-1);
-  if (n_tok == 0) return 0;
+  if (n_tok <= msa::rope::kSmallTokens) return 0;
   return static_cast<size_t>(shape->n_streams) * (shape->capacity / 128) * shape->n_kv_heads *
          sizeof(msa::rope::BlockNeed);
 }
@@ -1421,8 +1421,8 @@ int msa_kv_append_fp8(const msa_shape* shape, const msa_pages* pages, const msa_
   int64_t rows = 0;
   if ((st = pages_of(shape, pages, &P.pages, &rows)) != MSA_OK) return st;
   const size_t need = msa_kv_append_fp8_workspace_bytes(shape, n_tok);
-  if (workspace == nullptr || workspace_bytes < need) return MSA_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return MSA_ERR_ALIGN;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MSA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return MSA_ERR_ALIGN;
   const int G = shape->n_kv_heads;
   const int64_t units = static_cast<int64_t>(n_tok) * G;
   if (units >= (int64_t{1} << 31)) return MSA_ERR_RANGE;
@@ -1442,7 +1442,10 @@ int msa_kv_append_fp8(const msa_shape* shape, const msa_pages* pages, const msa_
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   constexpr int kWarps = msa::rope::kWarps;
   const dim3 block(kWarps * 32);
-  const dim3 grid(static_cast<unsigned>((units + kWarps - 1) / kWarps));
+  const dim3 grid(static_cast<unsigned>((n_tok + kWarps - 1) / kWarps));
+  if (need == 0)
+    return cuda_status(launch(msa::rope::fp8_append_small_kernel, dim3(static_cast<unsigned>(units)),
+                              dim3(msa::rope::kSmallWarps * 32), 0, s, P));
   const int64_t entries = static_cast<int64_t>(shape->n_streams) * (shape->capacity / 128) * G;
   if (cudaMemsetAsync(workspace, 0, need, s) != cudaSuccess) return MSA_ERR_CUDA;
   if (launch(msa::rope::fp8_need_kernel, grid, block, 0, s, P) != cudaSuccess) return MSA_ERR_CUDA;

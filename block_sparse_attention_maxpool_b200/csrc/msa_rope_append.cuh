@@ -11,7 +11,7 @@
 // float32 arithmetic, and one rounding to the stored type follows.
 //
 // Everything here is bound by its bytes (a prompt) or by launch latency (a
-// decode step).  One warp owns a (token, group) or a (query, group): a
+// decode step).  In the bf16 append one warp owns a (token, group) or a (query, group): a
 // token's K and V rows and its indexer key are one load each per lane, a
 // query's 16 heads are eight 16-byte loads per lane, all in flight before
 // the first is used.
@@ -316,12 +316,11 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t w, float ratio) {
   return to_e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 
-// One token's K row (lanes 0-15, turned) or V row (lanes 16-31): the lane's
-// two vectors of four values and where they start.
+// One token's K row (lanes 0-15) or V row (lanes 16-31): the lane's two
+// vectors of four values and where they start.
 __device__ __forceinline__ void load_kv(const Fp8Params& P, size_t src, int lane, float (&a)[4], float (&b)[4],
-                                        int& d0, int& d1, const float* cs, const float* sn) {
-  const int j = lane & 15;
-  vector_dims<4>(P.rope, j, d0, d1);
+                                        int& d0, int& d1) {
+  vector_dims<4>(P.rope, lane & 15, d0, d1);
   const __nv_bfloat16* from = (lane < 16 ? P.k_new : P.v_new) + src;
   const uint2 x = *reinterpret_cast<const uint2*>(from + d0);
   const uint2 y = *reinterpret_cast<const uint2*>(from + d1);
@@ -329,7 +328,6 @@ __device__ __forceinline__ void load_kv(const Fp8Params& P, size_t src, int lane
   a[2] = __uint_as_float(x.y << 16); a[3] = __uint_as_float(x.y & 0xffff0000u);
   b[0] = __uint_as_float(y.x << 16); b[1] = __uint_as_float(y.x & 0xffff0000u);
   b[2] = __uint_as_float(y.y << 16); b[3] = __uint_as_float(y.y & 0xffff0000u);
-  if (lane < 16) turn<4>(P.rope, j, a, b, cs, sn);
 }
 
 // Largest finite magnitude of the half-warp's row.
@@ -358,30 +356,37 @@ __device__ __forceinline__ long long fp8_block(const Fp8Params& P, int t, int g,
 }
 
 // 1 of 3: the scale every touched block needs (integer maxima: the order in
-// which tokens arrive does not matter).
+// which tokens arrive does not matter).  One warp per token: the table of its
+// angles serves all groups, four groups' rows are in flight at a time.
 __global__ void __launch_bounds__(kWarps * 32) fp8_need_kernel(const Fp8Params P) {
   __shared__ __align__(16) float table[kWarps][2][64];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (unit >= static_cast<long long>(P.n_tok) * P.G) return;
-  const int t = static_cast<int>(unit / P.G);
-  const int g = static_cast<int>(unit - static_cast<long long>(t) * P.G);
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= P.n_tok) return;
   int s, p;
-  if (fp8_block(P, t, g, s, p, lane, true) < 0) return;
+  if (fp8_block(P, t, 0, s, p, lane, true) < 0) return;
   float* cs = table[threadIdx.x >> 5][0];
   float* sn = table[threadIdx.x >> 5][1];
   fill_table(P.rope, p, cs, sn, lane);
-  float a[4], b[4];
-  int d0, d1;
-  load_kv(P, (static_cast<size_t>(t) * P.G + g) * 128, lane, a, b, d0, d1, cs, sn);
-  const unsigned int bits = scale_bits(row_amax(a, b));
-  BlockNeed* e = P.need + (static_cast<size_t>(s) * (P.capacity / 128) + p / 128) * P.G + g;
-  if ((lane & 15) == 0) {
-    unsigned int* slot = lane == 0 ? &e->k : &e->v;
-    if (*reinterpret_cast<volatile unsigned int*>(slot) < bits) atomicMax(slot, bits);
-    if (lane == 0 && (p & 127) == 0) e->fresh = 1u;
+  BlockNeed* e = P.need + (static_cast<size_t>(s) * (P.capacity / 128) + p / 128) * P.G;
+  for (int g0 = 0; g0 < P.G; g0 += 4) {
+    float a[4][4], b[4][4];
+    int d0, d1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_kv(P, (static_cast<size_t>(t) * P.G + min(g0 + i, P.G - 1)) * 128, lane, a[i], b[i], d0, d1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (lane < 16) turn<4>(P.rope, lane & 15, a[i], b[i], cs, sn);
+      const unsigned int bits = scale_bits(row_amax(a[i], b[i]));
+      if (g0 + i < P.G && (lane & 15) == 0) {
+        unsigned int* slot = lane == 0 ? &e[g0 + i].k : &e[g0 + i].v;
+        if (*reinterpret_cast<volatile unsigned int*>(slot) < bits) atomicMax(slot, bits);
+        if (lane == 0 && (p & 127) == 0) e[g0 + i].fresh = 1u;
+      }
+    }
   }
 }
 
@@ -408,41 +413,38 @@ __device__ __forceinline__ float next_scale(float held, bool fresh, unsigned int
   return after;
 }
 
-// 2 of 3: the touched blocks' scales, and their older rows requantised.  A
-// lane looks at one table entry, the warp works on the touched ones.
+// 2 of 3: the touched blocks' scales, and their older rows requantised.  One
+// table entry per lane; the warp then works on the blocks that have to be
+// requantised one after the other.
 __global__ void __launch_bounds__(kWarps * 32) fp8_scale_kernel(const Fp8Params P) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int nblk = P.capacity / 128;
   const long long n = static_cast<long long>(P.n_streams) * nblk * P.G;
-  const long long base = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * 32;
-  if (base >= n) return;
-  uint4 mine = make_uint4(0u, 0u, 0u, 0u);
-  if (base + lane < n) mine = *reinterpret_cast<const uint4*>(P.need + base + lane);
-  unsigned int todo = __ballot_sync(0xffffffffu, mine.x != 0u);
+  const long long e = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * 32 + lane;
+  long long row = -1;
+  float gk = 0.f, gv = 0.f;
+  if (e < n) {
+    const uint4 need = *reinterpret_cast<const uint4*>(P.need + e);
+    if (need.x != 0u) {
+      const int g = static_cast<int>(e % P.G);
+      const long long sb = e / P.G;
+      row = kv_block_row(P.pages, static_cast<int>(sb / nblk), g, static_cast<int>(sb % nblk), P.G, P.capacity);
+      if (row >= 0) {
+        P.k_scale[row / 128] = next_scale(P.k_scale[row / 128], need.z != 0u, need.x, gk);
+        P.v_scale[row / 128] = next_scale(P.v_scale[row / 128], need.z != 0u, need.y, gv);
+      }
+    }
+  }
+  unsigned int todo = __ballot_sync(0xffffffffu, gk != 0.f || gv != 0.f);
   while (todo != 0u) {
     const int l = __ffs(todo) - 1;
     todo &= todo - 1u;
-    const unsigned int nk = __shfl_sync(0xffffffffu, mine.x, l);
-    const unsigned int nv = __shfl_sync(0xffffffffu, mine.y, l);
-    const bool fresh = __shfl_sync(0xffffffffu, mine.z, l) != 0u;
-    const long long e = base + l;
-    const int g = static_cast<int>(e % P.G);
-    const long long sb = e / P.G;
-    const long long row = kv_block_row(P.pages, static_cast<int>(sb / nblk), g, static_cast<int>(sb % nblk), P.G,
-                                       P.capacity);
-    if (row < 0) continue;
-    float gk, gv;
-    const float sk = next_scale(P.k_scale[row / 128], fresh, nk, gk);
-    const float sv = next_scale(P.v_scale[row / 128], fresh, nv, gv);
-    __syncwarp();                              // every lane has read the old scales
-    if (gk != 0.f) requantise_block(P.k_cache, row, gk, lane, 32);
-    if (gv != 0.f) requantise_block(P.v_cache, row, gv, lane, 32);
-    if (lane == 0) {
-      P.k_scale[row / 128] = sk;
-      P.v_scale[row / 128] = sv;
-    }
+    const long long r = __shfl_sync(0xffffffffu, row, l);
+    const float fk = __shfl_sync(0xffffffffu, gk, l), fv = __shfl_sync(0xffffffffu, gv, l);
+    if (fk != 0.f) requantise_block(P.k_cache, r, fk, lane, 32);
+    if (fv != 0.f) requantise_block(P.v_cache, r, fv, lane, 32);
   }
 }
 
@@ -459,21 +461,123 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_store_kernel(const Fp8Params 
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (unit >= static_cast<long long>(P.n_tok) * P.G) return;
-  const int t = static_cast<int>(unit / P.G);
-  const int g = static_cast<int>(unit - static_cast<long long>(t) * P.G);
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= P.n_tok) return;
   int s, p;
-  const long long blk = fp8_block(P, t, g, s, p, lane, false);
-  if (blk < 0) return;
+  const long long blk0 = fp8_block(P, t, 0, s, p, lane, false);
+  if (blk0 < 0) return;
   float* cs = table[threadIdx.x >> 5][0];
   float* sn = table[threadIdx.x >> 5][1];
   fill_table(P.rope, p, cs, sn, lane);
+  for (int g0 = 0; g0 < P.G; g0 += 4) {
+    float a[4][4], b[4][4], scale[4];
+    long long blk[4];
+    int d0, d1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int g = min(g0 + i, P.G - 1);
+      blk[i] = kv_block_row(P.pages, s, g, p / 128, P.G, P.capacity);
+      load_kv(P, (static_cast<size_t>(t) * P.G + g) * 128, lane, a[i], b[i], d0, d1);
+      scale[i] = (lane < 16 ? P.k_scale : P.v_scale)[blk[i] / 128];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (lane < 16) turn<4>(P.rope, lane & 15, a[i], b[i], cs, sn);
+      if (g0 + i < P.G)
+        store_e4m3((lane < 16 ? P.k_cache : P.v_cache) + (static_cast<size_t>(blk[i]) + (p & 127)) * 128, a[i], b[i],
+                   d0, d1, scale[i]);
+    }
+  }
+}
+
+// The three steps in one launch, for calls of at most kSmallTokens tokens (a
+// decode step, a few drafted tokens): one CTA per (token, group).  The CTA of
+// the first token in the list that names a block looks the list over for the
+// others of that block and does all of them; the CTAs of the others leave.
+// With three launches and a cleared table 32 tokens took 28.8 us a call, and
+// the work of one launch is bound by its chain of dependent loads; the search
+// grows with the square of the tokens, so it is kept to short lists.
+constexpr int kSmallTokens = 256;
+constexpr int kSmallWarps = 4;
+
+__global__ void __launch_bounds__(kSmallWarps * 32) fp8_append_small_kernel(const Fp8Params P) {
+  __shared__ __align__(16) float table[kSmallWarps][2][64];
+  __shared__ unsigned int need_k, need_v, fresh, later;
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x / P.G;
+  const int g = blockIdx.x - t * P.G;
+  int s, p;
+  const long long blk = fp8_block(P, t, g, s, p, threadIdx.x, true);
+  if (blk < 0) return;
+  if (threadIdx.x == 0) {
+    need_k = need_v = 0u;
+    fresh = later = 0u;
+  }
+  // this thread's two tokens of the list: do they lie in the same block
+  static_assert(kSmallTokens == 2 * kSmallWarps * 32, "two tokens of the list per thread");
+  int pos[2];
+  bool same[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = i * kSmallWarps * 32 + threadIdx.x;
+    pos[i] = u < P.n_tok ? P.tok_pos[u] : -1;
+    same[i] = u < P.n_tok && P.tok_stream[u] == s && pos[i] >= 0 && pos[i] / 128 == p / 128;
+  }
+  const float held_k = P.k_scale[blk / 128], held_v = P.v_scale[blk / 128];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (same[i] && i * kSmallWarps * 32 + static_cast<int>(threadIdx.x) < t) later = 1u;
+  __syncthreads();
+  if (later != 0u) return;                     // an earlier token's CTA does this block
+  float* cs = table[warp][0];
+  float* sn = table[warp][1];
   float a[4], b[4];
-  int d0, d1;
-  load_kv(P, (static_cast<size_t>(t) * P.G + g) * 128, lane, a, b, d0, d1, cs, sn);
-  const float scale = (lane < 16 ? P.k_scale : P.v_scale)[blk / 128];
-  store_e4m3((lane < 16 ? P.k_cache : P.v_cache) + (static_cast<size_t>(blk) + (p & 127)) * 128, a, b, d0, d1, scale);
+  int d0 = 0, d1 = 0, last = -1;
+  // each warp does the tokens that its threads found, one after the other
+  auto each = [&](auto&& fn) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      unsigned int todo = __ballot_sync(0xffffffffu, same[i]);
+      while (todo != 0u) {
+        const int l = __ffs(todo) - 1;
+        todo &= todo - 1u;
+        const int u = i * kSmallWarps * 32 + warp * 32 + l;
+        const int q = __shfl_sync(0xffffffffu, pos[i], l);
+        if (u != last) {                       // (kept from the first pass where a warp has one token)
+          load_kv(P, (static_cast<size_t>(u) * P.G + g) * 128, lane, a, b, d0, d1);
+          __syncwarp();
+          fill_table(P.rope, q, cs, sn, lane);
+          if (lane < 16) turn<4>(P.rope, lane & 15, a, b, cs, sn);
+          last = u;
+        }
+        fn(q);
+      }
+    }
+  };
+  each([&](int q) {
+    const unsigned int bits = scale_bits(row_amax(a, b));
+    if (lane == 0) atomicMax(&need_k, bits);
+    if (lane == 16) atomicMax(&need_v, bits);
+    if (lane == 0 && (q & 127) == 0) fresh = 1u;
+  });
+  __syncthreads();
+  float gk, gv;
+  const float sk = next_scale(held_k, fresh != 0u, need_k, gk);
+  const float sv = next_scale(held_v, fresh != 0u, need_v, gv);
+  if (gk != 0.f) requantise_block(P.k_cache, blk, gk, threadIdx.x, kSmallWarps * 32);
+  if (gv != 0.f) requantise_block(P.v_cache, blk, gv, threadIdx.x, kSmallWarps * 32);
+  if (threadIdx.x == 0) {
+    P.k_scale[blk / 128] = sk;
+    P.v_scale[blk / 128] = sv;
+  }
+  __syncthreads();                             // the old rows are requantised before the new ones land
+  each([&](int q) {
+    store_e4m3((lane < 16 ? P.k_cache : P.v_cache) + (static_cast<size_t>(blk) + (q & 127)) * 128, a, b, d0, d1,
+               lane < 16 ? sk : sv);
+  });
 }
 
 }  // namespace rope

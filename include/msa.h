@@ -472,7 +472,7 @@ typedef uint8_t msa_e4m3;
  * So the result does not depend on the order of the tokens in the call.
  * Other conditions as for msa_kv_append.  workspace: at least
  * msa_kv_append_fp8_workspace_bytes(shape, n_tok) bytes, 16-byte aligned, its
- * contents need not be initialised. */
+ * contents need not be initialised (0 bytes, and NULL, for up to 256 tokens). */
 MSA_API int msa_kv_append_fp8(const msa_shape* shape, const msa_pages* pages, const msa_rope* rope,
                               msa_e4m3* k_cache, msa_e4m3* v_cache, float* k_scale, float* v_scale,
                               const msa_bf16* k_new, const msa_bf16* v_new, const int32_t* tok_stream,

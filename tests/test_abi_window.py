@@ -55,13 +55,14 @@ def test_rope_append_refusals(lib):
 
 
 def test_fp8_append_refusals(lib):
-    need = lib.msa_kv_append_fp8_workspace_bytes(GOOD.c(), 2)
+    need = lib.msa_kv_append_fp8_workspace_bytes(GOOD.c(), 257)
     assert need == 2 * 8 * 4 * 16
+    assert lib.msa_kv_append_fp8_workspace_bytes(GOOD.c(), 256) == 0
     assert lib.msa_kv_append_fp8_workspace_bytes(GOOD.c(), 0) == 0
     assert lib.msa_kv_append_fp8_workspace_bytes(BAD.c(), 2) == ctypes.c_size_t(-1).value
     assert lib.msa_kv_append_fp8_workspace_bytes(GOOD.c(), -1) == ctypes.c_size_t(-1).value
 
-    def call(shape=GOOD, rope=None, p=(FAKE,) * 6, tok=(FAKE, FAKE), n=2, ws=FAKE, wb=need, pages=None):
+    def call(shape=GOOD, rope=None, p=(FAKE,) * 6, tok=(FAKE, FAKE), n=257, ws=FAKE, wb=need, pages=None):
         return lib.msa_kv_append_fp8(shape.c(), pages, rope, *p, *tok, n, ws, wb, None)
     assert call(shape=BAD) == -3
     assert call(n=-1) == -4

@@ -45,10 +45,13 @@ def tokens(pattern, S, cap, gen):
         return [t[i] for i in torch.randperm(len(t), generator=gen)]
     if pattern == "draft":                        # a few consecutive slots per stream
         return [(s, p) for s in range(S) for p in range(126, 131)]
+    if pattern == "mixed":                        # a short list in any order, several tokens of a block apart in it
+        t = [(s, p) for s in range(S) for p in range(90, 160, 1 + s)]
+        return [t[i] for i in torch.randperm(len(t), generator=gen)]
     raise ValueError(pattern)
 
 
-@pytest.mark.parametrize("pattern", ["decode", "chunk", "shuffled", "draft"])
+@pytest.mark.parametrize("pattern", ["decode", "chunk", "shuffled", "draft", "mixed"])
 @pytest.mark.parametrize("G,paged,rope", [(4, False, None), (2, True, (64, False)), (1, True, (128, True)), (16, False, None)])
 def test_append(pattern, G, paged, rope):
     gen = torch.Generator().manual_seed(G + len(pattern))
