@@ -663,47 +663,51 @@ def msa_rope_append(shape: Shape, rope: Rope, k_cache=None, v_cache=None, k_new=
     keys (idx_k_cache: float32 or float16) and the queries q, idx_q are each
     optional.  Returns (q_out, idx_q_out), allocated here when None; pass an
     input as its output to rotate it in place."""
-    lead = next((t for t in (tok_pos, q_pos) if t is not None), None)
-    if lead is None:
+    if tok_pos is not None:
+        dev = _device_of(tok_pos, "tok_pos")
+    elif q_pos is not None:
+        dev = _device_of(q_pos, "q_pos")
+    else:
         raise ValueError("tok_pos or q_pos is required")
-    dev = _device_of(lead, "tok_pos" if tok_pos is not None else "q_pos")
     G, D, Di = shape.n_kv_heads, shape.head_dim, shape.idx_dim
-    nt = 0 if tok_pos is None else _n(tok_pos, "tok_pos")
-    nq = 0 if q_pos is None else _n(q_pos, "q_pos")
-    if (q is not None or idx_q is not None) and q_pos is None:
-        raise ValueError("q and idx_q need q_pos")
-    given = [t is not None for t in (k_cache, v_cache, k_new, v_new)]
-    if any(given) != all(given) or (idx_k_cache is None) != (idx_k_new is None):
+    kc = vc = kn = vn = ic = f16 = inew = ts = tp = qi = qo = iqi = iqo = qp = nt = nq = 0
+    kv, idx = k_cache is not None, idx_k_cache is not None
+    if (v_cache is not None) != kv or (k_new is not None) != kv or (v_new is not None) != kv or \
+            (idx_k_new is not None) != idx:
         raise ValueError("a cache and its new rows come together")
-    if (any(given) or idx_k_cache is not None) and (tok_stream is None or tok_pos is None):
-        raise ValueError("appended rows need tok_stream and tok_pos")
-    if q is None and idx_q is None:
-        nq = 0
-    if not any(given) and idx_k_cache is None:
-        nt = 0
-    if q is not None and q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if idx_q is not None and idx_q_out is None:
-        idx_q_out = torch.empty_like(idx_q, memory_format=torch.contiguous_format)
-    k = [0, 0, 0, 0, 0]
-    if any(given):
+    if kv or idx:
+        if tok_stream is None or tok_pos is None:
+            raise ValueError("appended rows need tok_stream and tok_pos")
+        nt = _n(tok_pos, "tok_pos")
+        ts = _dptr(tok_stream, torch.int32, (nt,), "tok_stream", dev)
+        tp = _dptr(tok_pos, torch.int32, (nt,), "tok_pos", dev)
+    if kv:
         cs, ns = _cache_shape(shape, pages, D), (nt, G, D)
-        k = [_dptr(k_cache, torch.bfloat16, cs, "k_cache", dev), _dptr(v_cache, torch.bfloat16, cs, "v_cache", dev),
-             _dptr(k_new, torch.bfloat16, ns, "k_new", dev), _dptr(v_new, torch.bfloat16, ns, "v_new", dev)]
-    ik = [0, 0, 0]
-    if idx_k_cache is not None:
-        kdt = torch.float16 if idx_k_cache.dtype == torch.float16 else torch.float32
-        ik = [_dptr(idx_k_cache, kdt, _cache_shape(shape, pages, Di), "idx_k_cache", dev), int(kdt == torch.float16),
-              _dptr(idx_k_new, torch.float32, (nt, G, Di), "idx_k_new", dev)]
-    tk = [0, 0] if nt == 0 else [_dptr(tok_stream, torch.int32, (nt,), "tok_stream", dev),
-                                 _dptr(tok_pos, torch.int32, (nt,), "tok_pos", dev)]
-    qs, iqs = (nq, shape.n_q_heads, D), (nq, G, Di)
-    qp = [0, 0] if q is None else [_dptr(q, torch.bfloat16, qs, "q", dev), _dptr(q_out, torch.bfloat16, qs, "q_out", dev)]
-    ip = [0, 0] if idx_q is None else [_dptr(idx_q, torch.float32, iqs, "idx_q", dev),
-                                       _dptr(idx_q_out, torch.float32, iqs, "idx_q_out", dev)]
-    pp = 0 if nq == 0 else _dptr(q_pos, torch.int32, (nq,), "q_pos", dev)
-    _launch("msa_rope_append", dev, (shape.c(), _pages_arg(shape, pages, dev), rope.c(dev), *k[:4], *ik, *tk, nt, *qp,
-                                     *ip, pp, nq, _on(dev, stream)))
+        kc, vc = _dptr(k_cache, torch.bfloat16, cs, "k_cache", dev), _dptr(v_cache, torch.bfloat16, cs, "v_cache", dev)
+        kn, vn = _dptr(k_new, torch.bfloat16, ns, "k_new", dev), _dptr(v_new, torch.bfloat16, ns, "v_new", dev)
+    if idx:
+        f16 = int(idx_k_cache.dtype is torch.float16)
+        ic = _dptr(idx_k_cache, torch.float16 if f16 else torch.float32, _cache_shape(shape, pages, Di), "idx_k_cache",
+                   dev)
+        inew = _dptr(idx_k_new, torch.float32, (nt, G, Di), "idx_k_new", dev)
+    if q is not None or idx_q is not None:
+        if q_pos is None:
+            raise ValueError("q and idx_q need q_pos")
+        nq = _n(q_pos, "q_pos")
+        qp = _dptr(q_pos, torch.int32, (nq,), "q_pos", dev)
+    if q is not None:
+        qs = (nq, shape.n_q_heads, D)
+        qi = _dptr(q, torch.bfloat16, qs, "q", dev)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        qo = _dptr(q_out, torch.bfloat16, qs, "q_out", dev)
+    if idx_q is not None:
+        iqi = _dptr(idx_q, torch.float32, (nq, G, Di), "idx_q", dev)
+        if idx_q_out is None:
+            idx_q_out = torch.empty_like(idx_q)
+        iqo = _dptr(idx_q_out, torch.float32, (nq, G, Di), "idx_q_out", dev)
+    _launch("msa_rope_append", dev, (shape.c(), _pages_arg(shape, pages, dev), rope.c(dev), kc, vc, kn, vn, ic, f16,
+                                     inew, ts, tp, nt, qi, qo, iqi, iqo, qp, nq, _on(dev, stream)))
     return q_out, idx_q_out
 
 

@@ -221,6 +221,9 @@ __global__ void __launch_bounds__(kThreads, Unit<kF8>::kCtas)
 
   const int qi = static_cast<int>(pair / P.G);
   const int g = static_cast<int>(pair - static_cast<long long>(qi) * P.G);
+  // the producer's selection is on its way with the query's place
+  int picked = -1;
+  if (!kWin && warp == kWarps) picked = __ldcg(P.sel + pair * kTopK + (lane & (kTopK - 1)));
   const int s = P.q_stream[qi];
   const int p = P.q_pos[qi];
   const bool valid_q = s >= 0 && s < P.n_streams && p >= 0 && p < P.capacity;
@@ -237,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, Unit<kF8>::kCtas)
     for (int base = u0; base < u1 && ok; base += 32) {
       int row = -1, lo = 0, hi = -1, sink = 0;
       float ks = 0.f, vs = 0.f;
+      const int block = kWin ? 0 : __shfl_sync(0xffffffffu, picked, ((base + lane) / (kBlock / kRows)) & (kTopK - 1));
       if (base + lane < u1) {
         const int u = base + lane;
         int first;
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, Unit<kF8>::kCtas)
           lo = max(0, p - P.window + 1 - first);
           sink = P.n_sink - first;
         } else {
-          const int b = __ldcg(P.sel + pair * kTopK + u / (kBlock / kRows));
+          const int b = block;
           any = b >= 0 && b <= p / kBlock;
           if (b > p / kBlock) raise_error(MSA_DEVERR_SEL_RANGE);
           first = b * kBlock + (u % (kBlock / kRows)) * kRows;
@@ -270,32 +274,34 @@ __global__ void __launch_bounds__(kThreads, Unit<kF8>::kCtas)
         const int r = __shfl_sync(0xffffffffu, row, i);
         const int l = __shfl_sync(0xffffffffu, lo, i), h = __shfl_sync(0xffffffffu, hi, i);
         const int sk = __shfl_sync(0xffffffffu, sink, i);
-        const float fk = __shfl_sync(0xffffffffu, ks, i), fv = __shfl_sync(0xffffffffu, vs, i);
+        const int st = k % kStages;
         if (lane == 0 && ok) {
-          const int st = k % kStages;
           if (k >= kStages) ok = mbar_wait(&empty[st], (k / kStages - 1) & 1);
-          if (ok) {
-            UnitInfo& in = info[st];
-            in.data = r >= 0;
-            in.lo = l;
-            in.hi = h;
-            in.sink = sk;
-            in.ks = fk;
-            in.vs = fv;
-            mbar_arrive_expect_tx(&full[st], r >= 0 ? kStageBytes : 0u);
-            if (r >= 0) {
-              uint8_t* dst = smem + st * kStageBytes;
-              if (kF8) {
-                tma_load_2d(dst, &tm_k, 0, r, &full[st]);
-                tma_load_2d(dst + kHalfStage, &tm_v, 0, r, &full[st]);
-              } else {
-                tma_load_2d(dst, &tm_k, 0, r, &full[st]);
-                tma_load_2d(dst + kHalfStage / 2, &tm_k, 64, r, &full[st]);
-                tma_load_2d(dst + kHalfStage, &tm_v, 0, r, &full[st]);
-                tma_load_2d(dst + kHalfStage + kHalfStage / 2, &tm_v, 64, r, &full[st]);
-              }
+          if (ok && r >= 0) {
+            uint8_t* dst = smem + st * kStageBytes;
+            if (kF8) {
+              tma_load_2d(dst, &tm_k, 0, r, &full[st]);
+              tma_load_2d(dst + kHalfStage, &tm_v, 0, r, &full[st]);
+            } else {
+              tma_load_2d(dst, &tm_k, 0, r, &full[st]);
+              tma_load_2d(dst + kHalfStage / 2, &tm_k, 64, r, &full[st]);
+              tma_load_2d(dst + kHalfStage, &tm_v, 0, r, &full[st]);
+              tma_load_2d(dst + kHalfStage + kHalfStage / 2, &tm_v, 64, r, &full[st]);
             }
           }
+        }
+        // the scales arrive behind the copies (the record's arrival closes the
+        // phase, so the copies may be announced after they were issued)
+        const float fk = __shfl_sync(0xffffffffu, ks, i), fv = __shfl_sync(0xffffffffu, vs, i);
+        if (lane == 0 && ok) {
+          UnitInfo& in = info[st];
+          in.data = r >= 0;
+          in.lo = l;
+          in.hi = h;
+          in.sink = sk;
+          in.ks = fk;
+          in.vs = fv;
+          mbar_arrive_expect_tx(&full[st], r >= 0 ? kStageBytes : 0u);
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;

@@ -358,13 +358,21 @@ __device__ __forceinline__ long long fp8_block(const Fp8Params& P, int t, int g,
 // 1 of 3: the scale every touched block needs (integer maxima: the order in
 // which tokens arrive does not matter).  One warp per token: the table of its
 // angles serves all groups, four groups' rows are in flight at a time.
-__global__ void __launch_bounds__(kWarps * 32) fp8_need_kernel(const Fp8Params P) {
+__global__ void __launch_bounds__(kWarps * 32, 4) fp8_need_kernel(const Fp8Params P) {
   __shared__ __align__(16) float table[kWarps][2][64];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= P.n_tok) return;
+  float a[4][4], b[4][4];
+  int d0, d1;
+  auto load4 = [&](int g0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_kv(P, (static_cast<size_t>(t) * P.G + min(g0 + i, P.G - 1)) * 128, lane, a[i], b[i], d0, d1);
+  };
+  load4(0);                                    // does not depend on where the token goes
   int s, p;
   if (fp8_block(P, t, 0, s, p, lane, true) < 0) return;
   float* cs = table[threadIdx.x >> 5][0];
@@ -372,18 +380,13 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_need_kernel(const Fp8Params P
   fill_table(P.rope, p, cs, sn, lane);
   BlockNeed* e = P.need + (static_cast<size_t>(s) * (P.capacity / 128) + p / 128) * P.G;
   for (int g0 = 0; g0 < P.G; g0 += 4) {
-    float a[4][4], b[4][4];
-    int d0, d1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_kv(P, (static_cast<size_t>(t) * P.G + min(g0 + i, P.G - 1)) * 128, lane, a[i], b[i], d0, d1);
+    if (g0 > 0) load4(g0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (lane < 16) turn<4>(P.rope, lane & 15, a[i], b[i], cs, sn);
       const unsigned int bits = scale_bits(row_amax(a[i], b[i]));
       if (g0 + i < P.G && (lane & 15) == 0) {
-        unsigned int* slot = lane == 0 ? &e[g0 + i].k : &e[g0 + i].v;
-        if (*reinterpret_cast<volatile unsigned int*>(slot) < bits) atomicMax(slot, bits);
+        atomicMax(lane == 0 ? &e[g0 + i].k : &e[g0 + i].v, bits);
         if (lane == 0 && (p & 127) == 0) e[g0 + i].fresh = 1u;
       }
     }
@@ -456,36 +459,42 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, const float (&a)[4], co
 }
 
 // 3 of 3: the call's rows.
-__global__ void __launch_bounds__(kWarps * 32) fp8_store_kernel(const Fp8Params P) {
+__global__ void __launch_bounds__(kWarps * 32, 4) fp8_store_kernel(const Fp8Params P) {
   __shared__ __align__(16) float table[kWarps][2][64];
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= P.n_tok) return;
+  float a[4][4], b[4][4];
+  int d0, d1;
+  auto load4 = [&](int g0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_kv(P, (static_cast<size_t>(t) * P.G + min(g0 + i, P.G - 1)) * 128, lane, a[i], b[i], d0, d1);
+  };
+  load4(0);
   int s, p;
   const long long blk0 = fp8_block(P, t, 0, s, p, lane, false);
   if (blk0 < 0) return;
+  // group g's block lies g blocks (pool) or g regions (contiguous cache) on
+  const long long step = P.pages.table != nullptr ? 128 : P.capacity;
+  const float* scales = lane < 16 ? P.k_scale : P.v_scale;
+  uint8_t* cache = lane < 16 ? P.k_cache : P.v_cache;
+  // lane 16 i + g holds the K (i = 0) or V scale of group g (G <= 16)
+  float mine = 0.f;
+  if ((lane & 15) < P.G) mine = scales[(blk0 + (lane & 15) * step) / 128];
   float* cs = table[threadIdx.x >> 5][0];
   float* sn = table[threadIdx.x >> 5][1];
   fill_table(P.rope, p, cs, sn, lane);
   for (int g0 = 0; g0 < P.G; g0 += 4) {
-    float a[4][4], b[4][4], scale[4];
-    long long blk[4];
-    int d0, d1;
+    if (g0 > 0) load4(g0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int g = min(g0 + i, P.G - 1);
-      blk[i] = kv_block_row(P.pages, s, g, p / 128, P.G, P.capacity);
-      load_kv(P, (static_cast<size_t>(t) * P.G + g) * 128, lane, a[i], b[i], d0, d1);
-      scale[i] = (lane < 16 ? P.k_scale : P.v_scale)[blk[i] / 128];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+      const float scale = __shfl_sync(0xffffffffu, mine, (lane & 16) + ((g0 + i) & 15));
       if (lane < 16) turn<4>(P.rope, lane & 15, a[i], b[i], cs, sn);
       if (g0 + i < P.G)
-        store_e4m3((lane < 16 ? P.k_cache : P.v_cache) + (static_cast<size_t>(blk[i]) + (p & 127)) * 128, a[i], b[i],
-                   d0, d1, scale[i]);
+        store_e4m3(cache + (static_cast<size_t>(blk0 + (g0 + i) * step) + (p & 127)) * 128, a[i], b[i], d0, d1, scale);
     }
   }
 }
