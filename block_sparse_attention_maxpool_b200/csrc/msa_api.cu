@@ -1099,11 +1099,37 @@ int make_map_8bit(CUtensorMap* m, const void* base, int64_t rows) {
   return r == CUDA_SUCCESS ? MSA_OK : MSA_ERR_CUDA;
 }
 
-// Prefill calls over an 8-bit cache expand it to bf16 first when a stream has
-// at least 64 queries on average; with fewer, the cluster kernel reads the
-// e4m3 rows directly.
+// Which kernel a prefill call takes.  The tensor-core tiles need queries that
+// share blocks, and enough of them: by the counts alone, since positions are
+// on the device.  A call with fewer than four queries per stream on average
+// (and than one wave of work) takes the cluster kernel, a (query, group) per
+// cluster.  Measured on 148 SMs, cluster kernel against tiles (us): bf16, 4
+// groups, window 1024: 64 queries 32 / 49, 128 47 / 48, 512 127 / 51; window
+// 128: 128 28 / 34, 512 60 / 34; 32 streams of 16 queries 129 / 52.
+bool tiles_pay(const msa_shape* sh, int32_t n_q) {
+  return static_cast<int64_t>(n_q) * sh->n_kv_heads >= 512 &&
+         static_cast<int64_t>(n_q) >= int64_t{4} * std::min(sh->n_streams, n_q);
+}
+
+// Prefill calls over an 8-bit cache expand it to bf16 before they take the
+// tiles, which wants more queries: window 1024: 64 queries 34 / 66, 256 77 /
+// 66; window 4096: 64 67 / 124, 256 190 / 128, 1024 675 / 216.
 bool expands(const msa_shape* sh, int32_t n_q, int mode, bool f8) {
-  return f8 && mode == MSA_MODE_PREFILL && static_cast<int64_t>(n_q) >= int64_t{64} * std::min(sh->n_streams, n_q);
+  return f8 && mode == MSA_MODE_PREFILL && static_cast<int64_t>(n_q) * sh->n_kv_heads >= 1024 &&
+         static_cast<int64_t>(n_q) >= int64_t{16} * std::min(sh->n_streams, n_q);
+}
+
+// Selected blocks: a tile of 8 queries reads the union of their selections,
+// about n (1 - (1 - 15 / n)^8) of n blocks where queries choose apart from one
+// another, one microsecond a block on 148 SMs; the cluster kernel reads each
+// query's 16 blocks, 0.085 us for a (query, group).  Measured (tiles /
+// cluster, us), 4 groups: 2048 queries on 4096 tokens 310 / 693, on 16384
+// 637 / 698, on 65536 841 / 700; 256 queries on 16384 161 / 107.
+bool selection_tiles_pay(const msa_shape* sh, int32_t n_q, int sms) {
+  const double nblk = sh->capacity / 128, pairs = static_cast<double>(n_q) * sh->n_kv_heads;
+  const double apart = nblk * (1.0 - std::pow(1.0 - std::min(1.0, 15.0 / nblk), 8.0));
+  const double waves = std::ceil(std::ceil(n_q / 8.0) * sh->n_kv_heads / sms);
+  return 70.0 + waves * apart < 10.0 + 0.085 * (148.0 / sms) * pairs * std::min(nblk, 16.0) / 16.0;
 }
 
 struct ExpandLayout {
@@ -1182,11 +1208,6 @@ int launch_cluster_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const 
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, P, k));
 }
 
-// Prefill calls of at least this many (16-query tile, group) tasks take the
-// tensor-core tiles; fewer leave most SMs without a tile, and the cluster
-// kernel spreads them better.
-constexpr int64_t kMinTileTasks = 8;
-
 int tile_attn(const msa_shape* sh, const msa_bf16* q, const void* k, const void* v, const msa::KvPages& pg, int64_t rows,
               const int32_t* q_stream, const int32_t* q_pos, int32_t n_q, int window, int n_sink, float softmax_scale,
               msa_bf16* out, int sms, cudaStream_t s) {
@@ -1249,7 +1270,7 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int window = std::min(a.window, sh->capacity);
   const int n_sink = std::min(a.n_sink, sh->capacity);
-  if (need > 0) {
+  if (need > 0 && (win || selection_tiles_pay(sh, n_q, sms))) {
     const ExpandLayout l = expand_layout(sh, n_q);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     msa::expand::Params E;
@@ -1284,8 +1305,7 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     return tile_attn(sh, q, E.k_out, E.v_out, msa::KvPages{E.table, static_cast<int>(blocks)}, blocks * G * 128,
                      q_stream, q_pos, n_q, window, n_sink, softmax_scale, out, sms, s);
   }
-  const int64_t tile_tasks = (static_cast<int64_t>(n_q) + msa::tattn::kTileQ - 1) / msa::tattn::kTileQ * G;
-  if (mode == MSA_MODE_PREFILL && !a.f8 && tile_tasks >= kMinTileTasks)
+  if (mode == MSA_MODE_PREFILL && !a.f8 && tiles_pay(sh, n_q))
     return tile_attn(sh, q, a.k_cache, a.v_cache, pg, rows, q_stream, q_pos, n_q, window, n_sink, softmax_scale, out,
                      sms, s);
   CUtensorMap tm_k, tm_v;

@@ -539,10 +539,11 @@ MSA_API int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages*
 /* Bytes of workspace that the window and 8-bit attention calls of `mode`
  * (MSA_MODE_DECODE, MSA_MODE_PREFILL) need for n_q queries over a bf16 or
  * (fp8 nonzero) an 8-bit cache; (size_t)-1 for an unsupported shape.  It is 0
- * except for prefill calls over an 8-bit cache with at least 64 queries per
- * stream on average: those expand the blocks that the call's queries can see
- * to bf16 in the workspace, which has room for the whole cache (512 bytes per
- * slot and group; one buffer serves all layers of a model in turn). */
+ * except for prefill calls over an 8-bit cache with many queries (1024
+ * (query, group) pairs, 16 queries per stream on average): those may expand
+ * the blocks that the call's queries can see to bf16 in the workspace, which
+ * has room for the whole cache (512 bytes per slot and group; one buffer
+ * serves all layers of a model in turn). */
 MSA_API size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode, int32_t fp8);
 
 /* msa_decode_step_fused - one whole decode step in a single persistent

@@ -23,9 +23,9 @@ U = 2.0 ** -24
 P_BF16, P_FP16 = 2.0 ** -8, 2.0 ** -11
 
 
-def norm_of(f8, mode, n, S):
-    """norm_round of a call: see check_attention (prefill calls with 64 queries per stream expand an 8-bit cache)."""
-    return P_FP16 if f8 and not (mode == "prefill" and n >= 64 * min(S, n)) else 0.0
+def norm_of(f8):
+    """norm_round of a call: see check_attention (prefill calls may or may not expand an 8-bit cache)."""
+    return P_FP16 if f8 else 0.0
 
 
 POISON = float("nan")

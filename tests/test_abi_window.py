@@ -111,13 +111,14 @@ def test_attention_refusals(lib, mode):
             assert call(kv=tuple(FAKE + 4 if j == i else FAKE for j in range(nkv))) == -2
         assert call(pages=msa.CPages(FAKE, -1)) == -4
         assert call(n=1 << 26, shape=msa.Shape(1, 128, 256, 16)) == -4
-        if f8 and mode == "prefill":           # 64 queries per stream: the cache is expanded to bf16
-            big = lib.msa_attn_workspace_bytes(GOOD.c(), 128, m, 1)
+        if f8 and mode == "prefill":           # many queries: the cache is expanded to bf16
+            big = lib.msa_attn_workspace_bytes(GOOD.c(), 256, m, 1)
             assert big >= 2 * 4 * 1024 * 512
-            assert lib.msa_attn_workspace_bytes(GOOD.c(), 127, m, 1) == 0
-            assert call(n=128, ws=0, wb=big) == -5
-            assert call(n=128, wb=big - 1) == -5
-            assert call(n=128, ws=FAKE + 128, wb=big) == -2
+            assert lib.msa_attn_workspace_bytes(GOOD.c(), 255, m, 1) == 0
+            assert lib.msa_attn_workspace_bytes(msa.Shape(64, 1024).c(), 1023, m, 1) == 0
+            assert call(n=256, ws=0, wb=big) == -5
+            assert call(n=256, wb=big - 1) == -5
+            assert call(n=256, ws=FAKE + 128, wb=big) == -2
     fn = getattr(lib, f"msa_sparse_attn_{mode}_fp8")
 
     def sparse(shape=GOOD, q=FAKE, kv=(FAKE,) * 4, sel=FAKE, n=2, sc=scale, ws=FAKE, wb=need):

@@ -191,8 +191,8 @@ def random_sel(n, G, pos, gen, nblk):
     (5, 2, 2176, 37, False, False),
     (2, 16, 640, 9, True, True),
     (1, 4, 2944, 150, True, True),
-    (2, 2, 2560, 300, False, False),
-    (3, 1, 1024, 500, True, True),
+    (2, 4, 2560, 400, False, False),
+    (3, 4, 1024, 500, True, True),
 ])
 def test_selected_attention(mode, S, G, cap, n, paged, pow2):
     gen = torch.Generator().manual_seed(S * cap + n)
@@ -228,8 +228,8 @@ def test_selected_attention(mode, S, G, cap, n, paged, pow2):
              pos.cuda(), out=out, pages=pages)
     assert got is out
     PW.device_error()
-    kv_round = 2.0 ** -8 if mode == "prefill" and not pow2 and n >= 64 * S else 0.0
-    print(f"\n[fp8 {mode}] of its bound: {PW.check_attention(got, want, spread, reach, PW.P_BF16, kv_round, PW.norm_of(True, mode, n, S)):.2f}")
+    kv_round = 2.0 ** -8 if mode == "prefill" and not pow2 else 0.0
+    print(f"\n[fp8 {mode}] of its bound: {PW.check_attention(got, want, spread, reach, PW.P_BF16, kv_round, PW.norm_of(True)):.2f}")
 
 
 @pytest.mark.parametrize("mode", ["decode", "prefill"])
@@ -240,7 +240,7 @@ def test_nothing_to_attend(mode):
     k8, ks = PW.quantise(torch.randn((3, 1, 128, 128), generator=gen))
     table = torch.tensor([[0, -1, 1, 2], [3, -2, 0, 1]], dtype=torch.int32)
     pages = msa.Pages(table.cuda(), 3)
-    times = 30 if mode == "prefill" else 1
+    times = 700 if mode == "prefill" else 1
     stream = torch.tensor([0, 2, -1, 0, 0, 0, 1] * times, dtype=torch.int32)
     pos = torch.tensor([511, 5, 5, 512, -1, 200, 130] * times, dtype=torch.int32)
     sel = torch.full((7, 1, 16), -1, dtype=torch.int32)
@@ -262,7 +262,7 @@ def test_decode_step_on_8bit_caches(prefill):
     """decode_step with 8-bit caches and rotation: the selection of the bf16 step's scores, attention within the bound
     of the oracle on the caches the step left; captured and replayed it gives the same bits."""
     gen = torch.Generator().manual_seed(21)
-    S, G, cap, new_n = 2, 2, 2560, 70 if prefill else 1
+    S, G, cap, new_n = 2, 2, 2560, 400 if prefill else 1
     shape = msa.Shape(S, cap, 32, G)
     rope = msa.Rope(freqs(64).cuda())
     had = caches(S, G, cap, gen, spread=False)
@@ -285,8 +285,9 @@ def test_decode_step_on_8bit_caches(prefill):
     PW.device_error()
     q, _ = msa.msa_rope_append(shape, rope, q=new["q"], q_pos=new["q_pos"])
     k, v = (C.fp8_values(c[x + "_cache"].cpu(), c[x + "_scale"].cpu()) for x in "kv")
-    want, spread, reach = C.selected_attention(q.cpu(), k, v, sel.cpu(), stream, pos, 128 ** -0.5)
-    PW.check_attention(out, want, spread, reach, PW.P_BF16, 0.0, PW.norm_of(True, "prefill" if prefill else "decode", n, S))
+    some = torch.arange(0, n, 17 if prefill else 1)                 # every query of a decode step, some of a prompt
+    want, spread, reach = C.selected_attention(q.cpu()[some], k, v, sel.cpu()[some], stream[some], pos[some], 128 ** -0.5)
+    PW.check_attention(out[some.cuda()], want, spread, reach, PW.P_BF16, 0.0, PW.norm_of(True))
     assert bool((n_sel >= 1).all())
     graph = msa.DecodeGraph(shape, fresh(), new, prefill=prefill, rope=rope)
     assert torch.equal(graph.replay(), out)
