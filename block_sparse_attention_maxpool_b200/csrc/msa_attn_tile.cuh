@@ -9,12 +9,21 @@
 // rows, A and B, which share every K and V block it loads; while the softmax
 // warps of one tile work, the tensor pipe works for the other.
 //
-//   S = Q K^T    M = 128 rows, N = 128 keys (tensor memory, f32)
+//   S = Q K^T    M = 128 rows, N = 64 keys (tensor memory, f32)
 //   P = exp2(f S - m) as bf16 pairs over S's columns, one thread per row
 //   O += P V     A from tensor memory, B = V from shared memory
 //
+// Tensor memory holds O of both tiles (128 columns each) and, per tile, two
+// buffers of 64 columns: the halves of a block.  While the softmax of one half
+// runs, the other half's P V and the next block's S run, so a tile's chain of
+// MMA, softmax, MMA with a barrier crossing each (about 230 cycles) is hidden.
+// With one buffer of 128 columns per tile, S of the next block had to wait
+// for P V of the whole last one: 952 us instead of 854 us for an 8192-token
+// prompt, window 4096, 64 heads, although an MMA of 64 columns costs 69 cycles
+// where one of 128 costs 64 to 77 (both read the 128 rows of Q).
+//
 // A row's reference m is raised (and its O rescaled in tensor memory) only
-// when a block's maximum passes it by more than 8 (log2 units), so rescaling
+// when a half's maximum passes it by more than 8 (log2 units), so rescaling
 // is rare and P stays below 2^8.  The row sum adds the rounded P values.
 //
 // Warps: 0 plans the tile's blocks and loads K, 1 loads Q and issues S, 2
@@ -34,9 +43,15 @@
 //
 // Hot code is kept short and the rare paths (a masked block, a raised
 // reference) out of line: with twelve warps in five roles the instruction
-// cache decides.  The same kernel with the rare paths inside the unrolled
-// loops took 1.37 ms for an 8192-token prompt with a window of 4096 (64
-// heads), 1.13 ms with them outside.
+// cache decides.  With the rare paths inside loops unrolled over 128 columns
+// the same prompt took 1.37 ms.  Measured for it now: 0.81 ms, 1.02 PFLOP/s of
+// visible products (0.62 of cuBLAS's measured burst).  Per block (both tiles)
+// the S issuer spends about 2150 cycles issuing and the P V issuer 900, so the
+// tensor pipe is what the loop comes closest to; exponentials take about 1750
+// of a softmax warp's 3600.  Measured and not kept: every fourth exponential on
+// the FMA pipes (no change), the two tiles taking turns at the special-
+// function units (slower by a quarter), P through shared memory (slower by a
+// tenth), reading the next record ahead (no change).
 #pragma once
 
 #include "msa_attn_prefill_union.cuh"
@@ -45,7 +60,6 @@
 namespace msa {
 namespace tattn {
 
-using uattn::add_bf16x2_f32;
 using uattn::cvt_bf16x2;
 using uattn::ex2_approx;
 using uattn::ffma2;
@@ -319,10 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto done_rec = [&](int r) { mbar_arrive(&B.rec_empty[r % kRecs]); };
 
-  // The softmax rows need registers that the other roles do not.  The shares
-  // of the warpgroups add up to the launch's: 88 + 2 * 208 = 3 * 168.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // ------------------------- planner and K loader -------------------------
       Planner pl{P, smem, B, lane};
@@ -572,7 +583,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 12) {
     // ---------------- softmax and output: one thread per (query, head) row ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // the S issuer negates q where the factor is negative; -inf (masked) times
     // a zero factor would be NaN
     const float f = fmaxf(fabsf(P.scale_log2), 1.17549435e-38f);
@@ -660,18 +670,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (raise) m_ref = mb;
             const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;       // nothing visible yet
             const float2 f2 = make_float2(f, f), nm2 = make_float2(neg_m, neg_m);
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            // (the row sum adds the rounded values, two at a time)
+            const float2 one2 = make_float2(1.f, 1.f);
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             float pk[kPart / 2];
 #pragma unroll
             for (int i = 0; i < kPart / 2; ++i) {
               const float2 y = ffma2(make_float2(s[2 * i], s[2 * i + 1]), f2, nm2);
               // a row whose query does not see the block keeps nothing of it
               const uint32_t pp = mine ? cvt_bf16x2(ex2_approx(y.x), ex2_approx(y.y)) : 0u;
-              acc[i & 3] = add_bf16x2_f32(pp, acc[i & 3]);
+              acc[i & 1] = ffma2(make_float2(__uint_as_float(pp << 16), __uint_as_float(pp & 0xffff0000u)), one2, acc[i & 1]);
               pk[i] = __uint_as_float(pp);
             }
             tmem_st32(sb, pk);
-            l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            l += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           } else {
             float z[16];
 #pragma unroll
