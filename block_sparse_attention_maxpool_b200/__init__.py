@@ -209,7 +209,7 @@ _SIGS.update({
                                                   _P]),
     "msa_window_attn_prefill_fp8": (ctypes.c_int, [_SH, _PG, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _Z,
                                                    _P]),
-    "msa_attn_workspace_bytes": (_Z, [_SH, _I, _I, _I]),
+    "msa_attn_workspace_bytes": (_Z, [_SH, _PG, _I, _I, _I]),
 })
 
 
@@ -741,9 +741,10 @@ def msa_kv_append_fp8(shape: Shape, k_cache, v_cache, k_scale, v_scale, k_new, v
         0 if workspace is None else workspace.numel(), _on(dev, stream)))
 
 
-def msa_attn_workspace_bytes(shape: Shape, n_q: int, mode: int, fp8: bool = False) -> int:
+def msa_attn_workspace_bytes(shape: Shape, n_q: int, mode: int, fp8: bool = False, pages: Pages | None = None) -> int:
     """Workspace of the window and 8-bit attention calls (0 but for prefill over an 8-bit cache)."""
-    v = library().msa_attn_workspace_bytes(shape.c(), n_q, mode, int(fp8))
+    pg = None if pages is None else CPages(0, pages.n_pages)
+    v = library().msa_attn_workspace_bytes(shape.c(), pg, n_q, mode, int(fp8))
     if v == ctypes.c_size_t(-1).value:
         raise MsaError("msa_attn_workspace_bytes", -3)
     return v
@@ -772,7 +773,7 @@ def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_
         kv = (_dptr(k_cache, torch.bfloat16, cs, "k_cache", dev), _dptr(v_cache, torch.bfloat16, cs, "v_cache", dev))
     wp = wb = 0
     if workspace is None and mode == MODE_PREFILL and k_scale is not None:
-        need = msa_attn_workspace_bytes(shape, n, mode, True)
+        need = msa_attn_workspace_bytes(shape, n, mode, True, pages)
         if need > 0:
             workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     if workspace is not None:

@@ -1133,25 +1133,23 @@ bool selection_tiles_pay(const msa_shape* sh, int32_t n_q, int sms) {
 }
 
 struct ExpandLayout {
-  size_t range, table, plans, k, v, total;
+  size_t range, plans, k, v, total;
 };
 
-ExpandLayout expand_layout(const msa_shape* sh, int32_t n_q) {
+// rows: of the cache or page pool.
+ExpandLayout expand_layout(const msa_shape* sh, int64_t rows, int32_t n_q) {
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t blocks = static_cast<size_t>(sh->n_streams) * (sh->capacity / 128);
   ExpandLayout l;
   l.range = 0;
-  l.table = up(static_cast<size_t>(sh->n_streams) * 2 * sizeof(int32_t));
-  l.plans = up(l.table + blocks * sizeof(int32_t));
+  l.plans = up(static_cast<size_t>(sh->n_streams) * 2 * sizeof(int32_t));
   l.k = up(l.plans + attn_workspace(sh, n_q, MSA_MODE_PREFILL));
-  const size_t pool = blocks * sh->n_kv_heads * 128 * 128 * sizeof(msa_bf16);
-  l.v = l.k + pool;
-  l.total = l.v + pool;
+  l.v = l.k + static_cast<size_t>(rows) * 128 * sizeof(msa_bf16);
+  l.total = l.v + static_cast<size_t>(rows) * 128 * sizeof(msa_bf16);
   return l;
 }
 
-size_t ext_attn_workspace(const msa_shape* sh, int32_t n_q, int mode, bool f8) {
-  return n_q > 0 && expands(sh, n_q, mode, f8) ? expand_layout(sh, n_q).total : 0;
+size_t ext_attn_workspace(const msa_shape* sh, int64_t rows, int32_t n_q, int mode, bool f8) {
+  return n_q > 0 && expands(sh, n_q, mode, f8) ? expand_layout(sh, rows, n_q).total : 0;
 }
 
 // What a window or 8-bit attention call attends to.
@@ -1205,7 +1203,12 @@ int launch_cluster_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = k > 1 ? 2 : 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, P, k));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tm_k, tm_v, P, k);
+  if (e != cudaSuccess && k > 8) {             // clusters of 16 are not portable: a part of a GPU may have none
+    cudaGetLastError();
+    return launch_cluster_attn<kF8, kWin>(tm_k, tm_v, P, n_pairs, 8, s);
+  }
+  return cuda_status(e);
 }
 
 int tile_attn(const msa_shape* sh, const msa_bf16* q, const void* k, const void* v, const msa::KvPages& pg, int64_t rows,
@@ -1259,8 +1262,7 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   msa::KvPages pg;
   int64_t rows = 0;
   if ((st = pages_of(sh, pages, &pg, &rows)) != MSA_OK) return st;
-  // (the selection tiles take a non-negative scale)
-  const size_t need = !win && softmax_scale < 0.f ? 0 : ext_attn_workspace(sh, n_q, mode, a.f8);
+  const size_t need = ext_attn_workspace(sh, rows, n_q, mode, a.f8);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return MSA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MSA_ERR_ALIGN;
@@ -1270,8 +1272,9 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int window = std::min(a.window, sh->capacity);
   const int n_sink = std::min(a.n_sink, sh->capacity);
-  if (need > 0 && (win || selection_tiles_pay(sh, n_q, sms))) {
-    const ExpandLayout l = expand_layout(sh, n_q);
+  // (the selection tiles take a positive scale)
+  if (need > 0 && (win || (softmax_scale > 0.f && selection_tiles_pay(sh, n_q, sms)))) {
+    const ExpandLayout l = expand_layout(sh, rows, n_q);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     msa::expand::Params E;
     E.k_cache = static_cast<const uint8_t*>(a.k_cache);
@@ -1280,7 +1283,6 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     E.v_scale = a.v_scale;
     E.k_out = reinterpret_cast<uint4*>(ws + l.k);
     E.v_out = reinterpret_cast<uint4*>(ws + l.v);
-    E.table = reinterpret_cast<int32_t*>(ws + l.table);
     E.range = reinterpret_cast<int32_t*>(ws + l.range);
     E.q_stream = q_stream;
     E.q_pos = q_pos;
@@ -1291,19 +1293,21 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     E.window = win ? window : sh->capacity;
     E.n_sink = n_sink;
     E.pages = pg;
-    const int64_t blocks = static_cast<int64_t>(sh->n_streams) * (sh->capacity / 128);
     if (cudaMemsetAsync(E.range, 0, static_cast<size_t>(sh->n_streams) * 2 * sizeof(int32_t), s) != cudaSuccess)
       return MSA_ERR_CUDA;
+    // about eight CTAs per SM, at most one per block of a stream and group
+    const int64_t sg = static_cast<int64_t>(sh->n_streams) * G;
+    const int64_t x = std::max<int64_t>(1, std::min<int64_t>(sh->capacity / 128, (8 * static_cast<int64_t>(sms) + sg - 1) / sg));
     if (launch(msa::expand::expand_range_kernel, dim3((n_q + 255) / 256), dim3(256), 0, s, E) != cudaSuccess ||
-        launch(msa::expand::expand_kernel, dim3(static_cast<unsigned>(blocks * G)), dim3(256), 0, s, E) != cudaSuccess)
+        launch(msa::expand::expand_kernel, dim3(static_cast<unsigned>(sh->n_streams), G,
+                                                static_cast<unsigned>(std::min<int64_t>(x, 65535))),
+               dim3(256), 0, s, E) != cudaSuccess)
       return MSA_ERR_CUDA;
-    const msa_pages mine{E.table, static_cast<int32_t>(blocks)};
     if (!win)
       return sparse_attn(sh, q, reinterpret_cast<const msa_bf16*>(E.k_out), reinterpret_cast<const msa_bf16*>(E.v_out),
                          a.sel, q_stream, q_pos, n_q, softmax_scale, out, ws + l.plans, l.k - l.plans, stream,
-                         MSA_MODE_PREFILL, &mine);
-    return tile_attn(sh, q, E.k_out, E.v_out, msa::KvPages{E.table, static_cast<int>(blocks)}, blocks * G * 128,
-                     q_stream, q_pos, n_q, window, n_sink, softmax_scale, out, sms, s);
+                         MSA_MODE_PREFILL, pages);
+    return tile_attn(sh, q, E.k_out, E.v_out, pg, rows, q_stream, q_pos, n_q, window, n_sink, softmax_scale, out, sms, s);
   }
   if (mode == MSA_MODE_PREFILL && !a.f8 && tiles_pay(sh, n_q))
     return tile_attn(sh, q, a.k_cache, a.v_cache, pg, rows, q_stream, q_pos, n_q, window, n_sink, softmax_scale, out,
@@ -1529,10 +1533,17 @@ int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages* pages, 
                      softmax_scale, out, workspace, workspace_bytes, stream, MSA_MODE_PREFILL);
 }
 
-size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode, int32_t fp8) {
+size_t msa_attn_workspace_bytes(const msa_shape* shape, const msa_pages* pages, int32_t n_q, int32_t mode,
+                                int32_t fp8) {
   if (check_shape(shape) != MSA_OK || n_q < 0 || (mode != MSA_MODE_DECODE && mode != MSA_MODE_PREFILL))
     return static_cast<size_t>(-1);
-  return ext_attn_workspace(shape, n_q, mode, fp8 != 0);
+  int64_t rows = static_cast<int64_t>(shape->n_streams) * shape->n_kv_heads * shape->capacity;
+  if (pages != nullptr) {
+    if (pages->n_pages <= 0) return static_cast<size_t>(-1);
+    rows = static_cast<int64_t>(pages->n_pages) * shape->n_kv_heads * 128;
+    if (rows >= (int64_t{1} << 31)) return static_cast<size_t>(-1);
+  }
+  return ext_attn_workspace(shape, rows, n_q, mode, fp8 != 0);
 }
 
 size_t msa_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode) {

@@ -2,15 +2,15 @@
 //
 // A prompt's tiles read a block many times (every 16 queries of a window read
 // it again, 8 queries of a selection share it at best), so the e4m3 values
-// are converted once per call, by a kernel of their own, into page pools in
-// the caller's workspace that the bf16 prefill kernels read through a page
-// table made here: bf16(scale * e4m3), exact when the scale is a power of
-// two, as the append writes it.  Only blocks that some query of the call can
-// see are touched.  Bound by bytes: 128 read and 256 written per row.
-// (Converted inside the attention kernel by four warps of its own, block by
-// block, the 2048-query selection on 16384 tokens took 1.04 ms and a window
-// of 1000 over 2 x 2001 queries 0.176 ms: the conversion of a block, about
-// 4000 cycles next to the softmax warps, paced the loop.)
+// are converted once per call, by a kernel of their own, into caches in the
+// caller's workspace with the 8-bit caches' layout (the same page table serves
+// both), which the bf16 prefill kernels read: bf16(scale * e4m3), exact when
+// the scale is a power of two, as the append writes it.  Only blocks that some
+// query of the call can see are touched.  Bound by bytes: 128 read and 256
+// written per row.  (Converted inside the attention kernel by four warps of
+// its own, block by block, the 2048-query selection on 16384 tokens took 1.04
+// ms instead of 0.66: the conversion of a block, about 4000 cycles next to the
+// softmax warps, paced the loop.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -25,9 +25,8 @@ struct Params {
   const uint8_t* v_cache;
   const float* k_scale;       // scale of cache row r: k_scale[r / 128]
   const float* v_scale;
-  uint4* k_out;               // [S * nblk][G][128][128] bf16
+  uint4* k_out;               // bf16, rows as in k_cache
   uint4* v_out;
-  int32_t* table;             // [S][nblk]: the expanded block's page, -1 without one
   int32_t* range;             // [S][2], zeroed: highest position + 1, capacity - lowest slot seen
   const int32_t* q_stream;
   const int32_t* q_pos;
@@ -71,44 +70,55 @@ __device__ __forceinline__ void expand16(const uint4& x, float f, uint4& a, uint
   b = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// One CTA per (stream, block, group).
+// The NaN codes (0x7f, 0xff) of four e4m3 values set to zero.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+  const uint32_t nan = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // bit 7 of each such byte
+  return w & ~((nan >> 7) * 0xffu);
+}
+
+// CTA (stream, group, z): blocks z, z + gridDim.z, ... of those that the
+// stream's queries see.
 __global__ void __launch_bounds__(256) expand_kernel(const Params P) {
   pdl_trigger();
   pdl_wait();
-  const int nblk = P.capacity / 128;
-  const long long sb = blockIdx.x / P.G;
-  const int g = static_cast<int>(blockIdx.x - sb * P.G);
-  const int s = static_cast<int>(sb / nblk), b = static_cast<int>(sb - static_cast<long long>(s) * nblk);
+  const int s = blockIdx.x, g = blockIdx.y;
   const int hi = P.range[2 * s], first = P.capacity - P.range[2 * s + 1];
-  const int j0 = b * 128;
-  if (j0 >= hi || (j0 + 127 < first && j0 >= P.n_sink)) return;   // nobody looks at its table entry either
-  const long long row = kv_block_row(P.pages, s, g, b, P.G, P.capacity);
-  if (g == 0 && threadIdx.x == 0) P.table[sb] = row < 0 ? -1 : static_cast<int32_t>(sb);
-  if (row < 0) return;
-  const float ks = P.k_scale[row / 128], vs = P.v_scale[row / 128];
-  const uint4* k = reinterpret_cast<const uint4*>(P.k_cache + row * 128);
-  const uint4* v = reinterpret_cast<const uint4*>(P.v_cache + row * 128);
-  uint4* ko = P.k_out + (sb * P.G + g) * (128 * 16);
-  uint4* vo = P.v_out + (sb * P.G + g) * (128 * 16);
-  uint4 x[4], y[4];
+  if (hi == 0) return;
+  const int win = first / 128;
+  const int sinks = min((P.n_sink + 127) / 128, win);
+  const int n = sinks + (hi - 1) / 128 - win + 1;
+  for (int i = blockIdx.z; i < n; i += gridDim.z) {
+    const int b = i < sinks ? i : win + i - sinks;
+    const long long row = kv_block_row(P.pages, s, g, b, P.G, P.capacity);
+    if (row < 0) continue;                       // the attention kernel reports it
+    const float ks = P.k_scale[row / 128], vs = P.v_scale[row / 128];
+    const uint4* k = reinterpret_cast<const uint4*>(P.k_cache + row * 128);
+    const uint4* v = reinterpret_cast<const uint4*>(P.v_cache + row * 128);
+    uint4* ko = P.k_out + row * 16;
+    uint4* vo = P.v_out + row * 16;
+    uint4 x[4], y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = __ldg(k + threadIdx.x + 256 * i);
-    y[i] = __ldg(v + threadIdx.x + 256 * i);
-  }
+    for (int c = 0; c < 4; ++c) {
+      x[c] = __ldg(k + threadIdx.x + 256 * c);
+      y[c] = __ldg(v + threadIdx.x + 256 * c);
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // rows that nobody sees become zeros (they may hold NaN)
-    const int j = j0 + (threadIdx.x + 256 * i) / 8;
-    if (j >= hi || (j < first && j >= P.n_sink)) x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
-    const int at = (threadIdx.x + 256 * i) * 2;
-    uint4 a, c;
-    expand16(x[i], ks, a, c);
-    ko[at] = a;
-    ko[at + 1] = c;
-    expand16(y[i], vs, a, c);
-    vo[at] = a;
-    vo[at + 1] = c;
+    for (int c = 0; c < 4; ++c) {
+      // V rows that no query of the stream sees may hold NaN, which times a
+      // weight of zero would still be NaN (other streams that share the page
+      // write the same values, but for such a NaN)
+      const int j = b * 128 + (threadIdx.x + 256 * c) / 8;
+      if (j >= hi || (j < first && j >= P.n_sink))
+        y[c] = make_uint4(without_nan(y[c].x), without_nan(y[c].y), without_nan(y[c].z), without_nan(y[c].w));
+      const int at = (threadIdx.x + 256 * c) * 2;
+      uint4 a, d;
+      expand16(x[c], ks, a, d);
+      ko[at] = a;
+      ko[at + 1] = d;
+      expand16(y[c], vs, a, d);
+      vo[at] = a;
+      vo[at + 1] = d;
+    }
   }
 }
 

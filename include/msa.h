@@ -465,14 +465,17 @@ typedef uint8_t msa_e4m3;
  *           the call writes there (at least 2^-100);
  *   after = max(before, need); before counts as empty when it is not
  *           positive, or when the call writes the block's first slot (the
- *           block starts anew, e.g. in a page that another sequence held);
+ *           block starts anew, e.g. in a page that another sequence held, and
+ *           what its other rows held is dropped: their bytes stay, but stand
+ *           for nothing under the new scale);
  *   rows already in the block are requantised from before to after when the
  *   scale grows, the call's rows are quantised with after (each to the nearest
  *   e4m3, ties to even; infinities become +-448, NaN stays NaN).
  * So the result does not depend on the order of the tokens in the call.
  * Other conditions as for msa_kv_append.  workspace: at least
  * msa_kv_append_fp8_workspace_bytes(shape, n_tok) bytes, 16-byte aligned, its
- * contents need not be initialised (0 bytes, and NULL, for up to 256 tokens). */
+ * contents need not be initialised (0 bytes, and NULL, for up to 256 tokens);
+ * calls that may run at the same time on the GPU need separate workspaces. */
 MSA_API int msa_kv_append_fp8(const msa_shape* shape, const msa_pages* pages, const msa_rope* rope,
                               msa_e4m3* k_cache, msa_e4m3* v_cache, float* k_scale, float* v_scale,
                               const msa_bf16* k_new, const msa_bf16* v_new, const int32_t* tok_stream,
@@ -489,7 +492,7 @@ MSA_API size_t msa_kv_append_fp8_workspace_bytes(const msa_shape* shape, int32_t
  * expands the cache (see msa_attn_workspace_bytes): exact for scales that are
  * powers of two, as msa_kv_append_fp8 writes them, else one more rounding.
  * pages may be NULL.  workspace: at least msa_attn_workspace_bytes(shape,
- * n_q, mode, 1) bytes, 256-byte aligned (NULL when that is 0). */
+ * pages, n_q, mode, 1) bytes, 256-byte aligned (NULL when that is 0). */
 MSA_API int msa_sparse_attn_decode_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
                                        const msa_e4m3* k_cache, const msa_e4m3* v_cache, const float* k_scale,
                                        const float* v_scale, const int32_t* sel, const int32_t* q_stream,
@@ -513,7 +516,7 @@ MSA_API int msa_sparse_attn_prefill_fp8(const msa_shape* shape, const msa_pages*
  * that a query sees can reach the other queries of its tile of 16.)  The _fp8
  * calls read an 8-bit cache, as msa_sparse_attn_decode_fp8 and
  * msa_sparse_attn_prefill_fp8 do.  pages may be NULL.  workspace: at least
- * msa_attn_workspace_bytes(shape, n_q, mode, fp8) bytes, 256-byte aligned
+ * msa_attn_workspace_bytes(shape, pages, n_q, mode, fp8) bytes, 256-byte aligned
  * (NULL when that is 0). */
 MSA_API int msa_window_attn_decode(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,
                                    const msa_bf16* k_cache, const msa_bf16* v_cache, const int32_t* q_stream,
@@ -538,13 +541,16 @@ MSA_API int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages*
 
 /* Bytes of workspace that the window and 8-bit attention calls of `mode`
  * (MSA_MODE_DECODE, MSA_MODE_PREFILL) need for n_q queries over a bf16 or
- * (fp8 nonzero) an 8-bit cache; (size_t)-1 for an unsupported shape.  It is 0
+ * (fp8 nonzero) an 8-bit cache, contiguous (pages NULL) or paged (only
+ * pages->n_pages is read); (size_t)-1 for unsupported arguments.  It is 0
  * except for prefill calls over an 8-bit cache with many queries (1024
  * (query, group) pairs, 16 queries per stream on average): those may expand
  * the blocks that the call's queries can see to bf16 in the workspace, which
- * has room for the whole cache (512 bytes per slot and group; one buffer
- * serves all layers of a model in turn). */
-MSA_API size_t msa_attn_workspace_bytes(const msa_shape* shape, int32_t n_q, int32_t mode, int32_t fp8);
+ * has room for the whole cache or pool (512 bytes per slot and group; one
+ * buffer serves all layers of a model in turn).  Calls that may run at the
+ * same time on the GPU need separate workspaces. */
+MSA_API size_t msa_attn_workspace_bytes(const msa_shape* shape, const msa_pages* pages, int32_t n_q, int32_t mode,
+                                        int32_t fp8);
 
 /* msa_decode_step_fused - one whole decode step in a single persistent
  * kernel: append the new tokens (msa_indexer_append + msa_kv_append), block

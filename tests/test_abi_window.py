@@ -81,11 +81,11 @@ def test_fp8_append_refusals(lib):
 @pytest.mark.parametrize("mode", ["decode", "prefill"])
 def test_attention_refusals(lib, mode):
     m = msa.MODE_PREFILL if mode == "prefill" else msa.MODE_DECODE
-    need = lib.msa_attn_workspace_bytes(GOOD.c(), 2, m, 1)
-    assert need == lib.msa_attn_workspace_bytes(GOOD.c(), 200, m, 0) == 0
-    assert lib.msa_attn_workspace_bytes(BAD.c(), 2, m, 0) == ctypes.c_size_t(-1).value
-    assert lib.msa_attn_workspace_bytes(GOOD.c(), -2, m, 0) == ctypes.c_size_t(-1).value
-    assert lib.msa_attn_workspace_bytes(GOOD.c(), 2, 2, 1) == ctypes.c_size_t(-1).value
+    need = lib.msa_attn_workspace_bytes(GOOD.c(), None, 2, m, 1)
+    assert need == lib.msa_attn_workspace_bytes(GOOD.c(), None, 200, m, 0) == 0
+    assert lib.msa_attn_workspace_bytes(BAD.c(), None, 2, m, 0) == ctypes.c_size_t(-1).value
+    assert lib.msa_attn_workspace_bytes(GOOD.c(), None, -2, m, 0) == ctypes.c_size_t(-1).value
+    assert lib.msa_attn_workspace_bytes(GOOD.c(), None, 2, 2, 1) == ctypes.c_size_t(-1).value
     scale = ctypes.c_float(0.1)
     for f8 in (False, True):
         fn = getattr(lib, f"msa_window_attn_{mode}" + ("_fp8" if f8 else ""))
@@ -112,10 +112,12 @@ def test_attention_refusals(lib, mode):
         assert call(pages=msa.CPages(FAKE, -1)) == -4
         assert call(n=1 << 26, shape=msa.Shape(1, 128, 256, 16)) == -4
         if f8 and mode == "prefill":           # many queries: the cache is expanded to bf16
-            big = lib.msa_attn_workspace_bytes(GOOD.c(), 256, m, 1)
+            big = lib.msa_attn_workspace_bytes(GOOD.c(), None, 256, m, 1)
             assert big >= 2 * 4 * 1024 * 512
-            assert lib.msa_attn_workspace_bytes(GOOD.c(), 255, m, 1) == 0
-            assert lib.msa_attn_workspace_bytes(msa.Shape(64, 1024).c(), 1023, m, 1) == 0
+            assert lib.msa_attn_workspace_bytes(GOOD.c(), None, 255, m, 1) == 0
+            assert lib.msa_attn_workspace_bytes(msa.Shape(64, 1024).c(), None, 1023, m, 1) == 0
+            assert 5 * 4 * 128 * 512 <= lib.msa_attn_workspace_bytes(GOOD.c(), msa.CPages(0, 5), 256, m, 1) < big
+            assert lib.msa_attn_workspace_bytes(GOOD.c(), msa.CPages(0, 0), 256, m, 1) == ctypes.c_size_t(-1).value
             assert call(n=256, ws=0, wb=big) == -5
             assert call(n=256, wb=big - 1) == -5
             assert call(n=256, ws=FAKE + 128, wb=big) == -2

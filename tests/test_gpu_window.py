@@ -303,3 +303,61 @@ def test_far_apart_scales(spread_v):
         got = run("decode", shape, q, kv, stream, pos, window, 4, poison=False)
         PW.check_attention(got, want, spread, reach, PW.P_BF16, 0.0, PW.P_FP16)
     PW.device_error()
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("f8", [False, True])
+def test_streams_that_share_pages(mode, f8):
+    """Two streams on the same prefix pages, one of them ending inside a shared page: each sees its own rows, also where
+    an 8-bit pool is expanded by both."""
+    gen = torch.Generator().manual_seed(19)
+    G, cap = 4, 512
+    shape = msa.Shape(2, cap, 16 * G, G)
+    kv = make(1, G, cap, f8, gen)                                    # one sequence's rows; both streams map its pages
+    table = torch.tensor([[2, 0, -1, -1], [2, 0, 3, 1]], dtype=torch.int32)
+    args = []
+    for x, sc, _ in kv:
+        raw = (x.view(torch.uint8) if f8 else x)
+        pool = torch.full((4, G, 128, 128), 0x7f if f8 else math.nan, dtype=raw.dtype)
+        scp = torch.full((4, G), math.nan)
+        for b in range(4):
+            pool[int(table[1, b])] = raw[0, :, b * 128:b * 128 + 128]
+            if f8:
+                scp[int(table[1, b])] = sc[0, :, b]
+        args.append((pool.cuda().view(F8) if f8 else pool.cuda(), scp.cuda() if f8 else None))
+    n = 300 if mode == "prefill" else 2
+    stream = (torch.arange(n) * 2 // n).int()
+    pos = torch.where(stream == 0, 30 + torch.arange(n) % 150, 511 - torch.arange(n) % 400).int()
+    q = torch.randn((n, 16 * G, 128), generator=gen).bfloat16()
+    both = [torch.cat((x, x)) for _, _, x in kv]
+    want = C.window_attention(q, *both, stream, pos, 100, 4, 128 ** -0.5)
+    for _ in range(3):
+        got = attend(mode, shape, q.cuda(), args[0][0], args[1][0], stream.cuda(), pos.cuda(), 100, 4,
+                     pages=msa.Pages(table.cuda(), 4), k_scale=args[0][1], v_scale=args[1][1])
+        PW.check_attention(got, *want, PW.P_BF16, 0.0, PW.norm_of(f8))
+    PW.device_error()
+
+
+def test_wrong_arguments_are_refused():
+    shape = msa.Shape(1, 256, 16, 1)
+    q = torch.zeros((1, 16, 128), dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros((1, 1, 256, 128), dtype=torch.bfloat16, device="cuda")
+    k8 = torch.zeros((1, 1, 256, 128), dtype=torch.uint8, device="cuda").view(F8)
+    sc = torch.ones((1, 1, 2), device="cuda")
+    t = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = dict(window=4)
+    for fn in (msa.msa_window_attn_decode, msa.msa_window_attn_prefill):
+        fn(shape, q, kv, kv, t, t, **good)
+        for bad in (dict(q=q[:, :8].contiguous()), dict(k=kv[:, :, :128].contiguous()), dict(v=kv.float()),
+                    dict(k=kv.transpose(2, 3)), dict(s=t.long()), dict(p=t.cpu()), dict(k=k8), dict(k=k8, v=k8),
+                    dict(scales=(sc, sc)), dict(k=k8, v=k8, scales=(sc[..., :1].contiguous(), sc)),
+                    dict(k=k8, v=kv, scales=(sc, sc))):
+            a = dict(q=q, k=kv, v=kv, s=t, p=t, scales=(None, None))
+            a.update(bad)
+            with pytest.raises(ValueError):
+                fn(shape, a["q"], a["k"], a["v"], a["s"], a["p"], 4, k_scale=a["scales"][0], v_scale=a["scales"][1])
+        for w, s in ((0, 0), (-3, 0), (4, -1)):
+            with pytest.raises(msa.MsaError):
+                fn(shape, q, kv, kv, t, t, w, s)
+    assert msa.msa_window_attn_decode(shape, q[:0], kv, kv, t[:0], t[:0], 4).shape == (0, 16, 128)
+    PW.device_error()
