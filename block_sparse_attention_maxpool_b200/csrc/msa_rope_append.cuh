@@ -14,7 +14,8 @@
 // decode step).  In the bf16 append one warp owns a (token, group) or a (query, group): a
 // token's K and V rows and its indexer key are one load each per lane, a
 // query's 16 heads are eight 16-byte loads per lane, all in flight before
-// the first is used.
+// the first is used.  16384 tokens with 64 query heads and indexer rows (738
+// MB): 130 us, 5.7 TB/s, 0.86 of the measured copy rate; 32 tokens: 5.4 us.
 #pragma once
 
 #include <cuda_fp16.h>
