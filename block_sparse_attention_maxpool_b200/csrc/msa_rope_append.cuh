@@ -408,12 +408,13 @@ __device__ __forceinline__ void requantise_block(uint8_t* cache, long long row, 
 }
 
 // New scale of a touched block from the old one; `grow`: the old rows' ratio
-// when they have to be requantised, else 0.
+// when they have to be requantised, else 0 (a ratio that float32 cannot hold
+// is taken as 2^-126, which makes zeros of any e4m3 as well).
 __device__ __forceinline__ float next_scale(float held, bool fresh, unsigned int need_bits, float& grow) {
   const float before = !fresh && held > 0.f ? held : 0.f;
   const float need = __uint_as_float(need_bits);
   const float after = fmaxf(before, need);
-  grow = before > 0.f && after > before ? before / after : 0.f;
+  grow = before > 0.f && after > before ? fmaxf(before / after, 1.17549435e-38f) : 0.f;
   return after;
 }
 

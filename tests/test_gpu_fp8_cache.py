@@ -153,6 +153,28 @@ def test_extreme_values():
     PW.device_error()
 
 
+@pytest.mark.parametrize("n", [1, 300])
+def test_scale_growing_past_float32(n):
+    """The old scale over the new one is below any float32: the older rows become zeros, not values of the new scale."""
+    G, cap = 2, 512
+    shape = msa.Shape(1, cap, 32, G)
+    had = {"k": torch.zeros((1, G, cap, 128), dtype=torch.uint8), "ks": torch.zeros((1, G, 4))}
+    had["k"][0, :, 1:5] = torch.tensor([0x7e, 0xfe, 0x38, 0x01], dtype=torch.uint8)[:, None]
+    had["ks"][0, :, 0] = 2.0 ** -90
+    pos = torch.arange(5, 5 + n, dtype=torch.int32)
+    stream = torch.zeros(n, dtype=torch.int32)
+    new = torch.full((n, G, 128), 2.0 ** 120).bfloat16()
+    want, ws = C.fp8_append(had["k"].view(F8).double(), had["ks"], new.double(), stream, pos)
+    assert not bool(want[0, :, 1:5].any()) and bool((ws[0, :, 0] == 2.0 ** 112).all())
+    k, v = had["k"].cuda().view(F8), had["k"].cuda().view(F8)
+    ks, vs = had["ks"].cuda(), had["ks"].cuda()
+    msa.msa_kv_append_fp8(shape, k, v, ks, vs, new.cuda(), new.cuda(), stream.cuda(), pos.cuda())
+    PW.device_error()
+    for got, scale in ((k, ks), (v, vs)):
+        assert torch.equal(scale.cpu().double(), ws)
+        assert torch.equal(got.cpu().double(), want)
+
+
 def test_skipped_tokens():
     shape = msa.Shape(2, 256, 16, 1)
     table = torch.tensor([[0, -1], [9, 1]], dtype=torch.int32)
