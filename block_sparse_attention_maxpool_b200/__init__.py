@@ -615,6 +615,15 @@ def _on(dev: int, stream) -> int:
     return _stream(stream)
 
 
+def _held(t: torch.Tensor, dev: int, stream) -> torch.Tensor:
+    """Tie memory allocated here (on the current stream) to the stream the call
+    launches on, so that it is not reused before that stream is done with it."""
+    if stream is not None:
+        raw = _stream(stream)
+        t.record_stream(torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev))
+    return t
+
+
 def _launch(fn: str, dev: int, args) -> None:
     """Call ``fn`` with ``dev`` as the current device (the library launches on it)."""
     f = getattr(_lib or library(), fn)
@@ -699,12 +708,12 @@ def msa_rope_append(shape: Shape, rope: Rope, k_cache=None, v_cache=None, k_new=
         qs = (nq, shape.n_q_heads, D)
         qi = _dptr(q, torch.bfloat16, qs, "q", dev)
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _held(torch.empty_like(q), dev, stream)
         qo = _dptr(q_out, torch.bfloat16, qs, "q_out", dev)
     if idx_q is not None:
         iqi = _dptr(idx_q, torch.float32, (nq, G, Di), "idx_q", dev)
         if idx_q_out is None:
-            idx_q_out = torch.empty_like(idx_q)
+            idx_q_out = _held(torch.empty_like(idx_q), dev, stream)
         iqo = _dptr(idx_q_out, torch.float32, (nq, G, Di), "idx_q_out", dev)
     _launch("msa_rope_append", dev, (shape.c(), _pages_arg(shape, pages, dev), rope.c(dev), kc, vc, kn, vn, ic, f16,
                                      inew, ts, tp, nt, qi, qo, iqi, iqo, qp, nq, _on(dev, stream)))
@@ -730,7 +739,7 @@ def msa_kv_append_fp8(shape: Shape, k_cache, v_cache, k_scale, v_scale, k_new, v
     need = 0
     if workspace is None:
         need = msa_kv_append_fp8_workspace_bytes(shape, n)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need > 0 else None
+        workspace = _held(torch.empty((need,), dtype=torch.uint8, device=dev), dev, stream) if need > 0 else None
     _launch("msa_kv_append_fp8", dev, (
         shape.c(), _pages_arg(shape, pages, dev), None if rope is None else rope.c(dev),
         _dptr(k_cache, torch.float8_e4m3fn, cs, "k_cache", dev), _dptr(v_cache, torch.float8_e4m3fn, cs, "v_cache", dev),
@@ -757,7 +766,7 @@ def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_
     qs = (n, shape.n_q_heads, shape.head_dim)
     qp = _dptr(q, torch.bfloat16, qs, "q", dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _held(torch.empty_like(q), dev, stream)
     cs = _cache_shape(shape, pages, shape.head_dim)
     if k_cache.dtype is torch.float8_e4m3fn:
         if k_scale is None or v_scale is None:
@@ -775,7 +784,7 @@ def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_
     if workspace is None and mode == MODE_PREFILL and k_scale is not None:
         need = msa_attn_workspace_bytes(shape, n, mode, True, pages)
         if need > 0:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            workspace = _held(torch.empty((need,), dtype=torch.uint8, device=dev), dev, stream)
     if workspace is not None:
         wp, wb = _dptr(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel()
     if softmax_scale is None:

@@ -260,6 +260,59 @@ def test_two_calls_at_once():
     assert all(torch.equal(x, want) for x in got[0] + got[1])
 
 
+@pytest.mark.parametrize("form", ["window", "append", "rope", "decode_step"])
+def test_memory_of_a_call_on_another_stream(form):
+    """A call launched on another stream than the current one: memory that it allocated for itself is not handed out
+    again while its kernels are still waiting there."""
+    S, G, cap, n = 2, 4, 2048, 2048
+    shape = msa.Shape(S, cap, 64, G)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    stream = (torch.arange(n, device="cuda") * S // n).int()
+    pos = (torch.arange(n, device="cuda") % (n // S) + 500).int()
+    randn = lambda *d, t=torch.bfloat16: torch.randn(d, device="cuda", generator=gen).to(t)
+    new = dict(tok_stream=stream, tok_pos=pos, q_stream=stream, q_pos=pos, k_new=randn(n, G, 128), v_new=randn(n, G, 128),
+               q=randn(n, 64, 128), idx_k_new=randn(n, G, 128, t=torch.float32), idx_q=randn(n, G, 128, t=torch.float32))
+    rope = msa.Rope(10000.0 ** (-torch.arange(64, dtype=torch.float64, device="cuda") / 64))
+
+    def call(side):
+        caches = msa.fp8_caches(shape, "cuda")
+        for c, size in (("k", 0x60), ("v", 0x48)):
+            caches[c + "_cache"].view(torch.uint8).copy_(torch.arange(S * G * cap * 128, device="cuda").view(S, G, cap, 128)
+                                                         * 37 % size)
+            caches[c + "_scale"].fill_(2.0 ** -6)
+        caches["idx_k_cache"] = torch.zeros((S, G, cap, 128), device="cuda")
+        torch.cuda.synchronize()
+        if side is not None:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+        out = torch.zeros_like(new["q"])
+        bufs = {"out": out, "workspace": torch.zeros(msa.msa_workspace_bytes(shape, n, msa.MODE_PREFILL), dtype=torch.uint8,
+                                                     device="cuda"),
+                "block_scores": torch.zeros((n, G, cap // 128), device="cuda")}
+        torch.cuda.synchronize() if side is None else torch.cuda.current_stream().synchronize()
+        if form == "window":
+            msa.msa_window_attn_prefill(shape, new["q"], caches["k_cache"], caches["v_cache"], stream, pos, 300, 4, out=out,
+                                        stream=side, k_scale=caches["k_scale"], v_scale=caches["v_scale"])
+        elif form == "append":
+            msa.msa_kv_append_fp8(shape, caches["k_cache"], caches["v_cache"], caches["k_scale"], caches["v_scale"],
+                                  new["k_new"], new["v_new"], stream, pos, rope, stream=side)
+        elif form == "rope":
+            msa.window_step(shape, caches, new, 300, 4, {"out": out}, side, True, None, rope)
+        else:
+            kept = msa.decode_step(shape, caches, new, bufs, side, True, None, rope)     # noqa: F841 (sel, n_sel)
+        # everything that the call let go of, taken again and overwritten at once
+        junk = [torch.full((m,), 1, dtype=torch.uint8, device="cuda") for k in range(8, 27) for m in (1 << k,) * 3]
+        torch.cuda.synchronize()
+        PW.device_error()
+        del junk
+        return [out] + [caches[c].view(torch.uint8) for c in ("k_cache", "v_cache")] + [caches["k_scale"], caches["v_scale"]]
+
+    want = call(None)
+    got = call(torch.cuda.Stream())
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_large_offsets():
     """A pool of more than 2^31 bytes: pages beyond 32-bit byte offsets."""
     gen = torch.Generator().manual_seed(4)
