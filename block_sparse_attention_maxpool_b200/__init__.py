@@ -551,7 +551,8 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
     With ``rope`` the new keys and the queries (idx_k_new, k_new, idx_q, q)
     arrive unrotated and are rotated on the way (bufs: q_rot, idx_q_rot).
     k_cache and v_cache may be 8-bit (float8_e4m3fn, with k_scale and v_scale
-    in ``caches``; bufs: workspace_fp8).
+    in ``caches``; bufs: workspace_fp8 for the append, workspace_attn for the
+    attention).
     Returns (out, sel, n_sel, block_scores).
     """
     b = bufs or {}
@@ -578,7 +579,7 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
         sel, n_sel = msa_select_topk(shape, bs, new["q_pos"], b.get("sel"), b.get("n_sel"), stream)
         attend = msa_sparse_attn_prefill_fp8 if prefill else msa_sparse_attn_decode_fp8
         out = attend(shape, new["q"], caches["k_cache"], caches["v_cache"], caches["k_scale"], caches["v_scale"], sel,
-                     new["q_stream"], new["q_pos"], None, b.get("out"), None, stream, pages)
+                     new["q_stream"], new["q_pos"], None, b.get("out"), b.get("workspace_attn"), stream, pages)
         return out, sel, n_sel, bs
     if not prefill:                         # the top-16 inside the attention kernel
         out, sel, n_sel = msa_select_attn_decode(shape, bs, new["q"], caches["k_cache"], caches["v_cache"],
@@ -594,6 +595,8 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
 # ---- rotating appends, 8-bit caches, window attention ---------------------------
 def _dptr(t: torch.Tensor, dtype, shape, name: str, dev: int) -> int:
     """_ptr of a tensor that has to be on CUDA device ``dev``, the call's device."""
+    if t is None:
+        raise ValueError(f"{name} is required")
     if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     p = _ptr(t, dtype, shape, name)
@@ -731,7 +734,8 @@ def msa_kv_append_fp8(shape: Shape, k_cache, v_cache, k_scale, v_scale, k_new, v
                       rope: Rope | None = None, workspace=None, stream=None, pages: Pages | None = None) -> None:
     """Write new K rows (rotated when ``rope`` is given) and V rows into 8-bit
     caches (float8_e4m3fn) with one scale per (128-token block, group);
-    a block whose scale grows has its older rows requantised."""
+    a block whose scale grows has its older rows requantised.  Two streams
+    whose tables name one page must not both write it in a call."""
     n = _n(tok_pos, "tok_pos")
     dev = _device_of(tok_pos, "tok_pos")
     cs, ss = _cache_shape(shape, pages, shape.head_dim), _scale_shape(shape, pages)
@@ -820,6 +824,11 @@ def msa_sparse_attn_prefill_fp8(shape: Shape, q, k_cache, v_cache, k_scale, v_sc
                        q_stream, q_pos, softmax_scale, out, workspace, stream, pages)
 
 
+def _window(shape: Shape, window: int, n_sink: int) -> tuple:
+    """(window, n_sink) as the library's int32; beyond the capacity they mean no more than the capacity does."""
+    return min(window, shape.capacity), min(n_sink, shape.capacity)
+
+
 def msa_window_attn_decode(shape: Shape, q, k_cache, v_cache, q_stream, q_pos, window: int, n_sink: int = 0,
                            softmax_scale=None, out=None, workspace=None, stream=None, pages: Pages | None = None,
                            k_scale=None, v_scale=None):
@@ -827,7 +836,7 @@ def msa_window_attn_decode(shape: Shape, q, k_cache, v_cache, q_stream, q_pos, w
     ``n_sink`` ones, for a few queries (decode).  The caches are bfloat16, or
     float8_e4m3fn with their k_scale and v_scale."""
     return _ext_attn("msa_window_attn_decode", MODE_DECODE, shape, q, k_cache, v_cache, k_scale, v_scale, (), q_stream,
-                     q_pos, (window, n_sink), softmax_scale, out, workspace, stream, pages)
+                     q_pos, _window(shape, window, n_sink), softmax_scale, out, workspace, stream, pages)
 
 
 def msa_window_attn_prefill(shape: Shape, q, k_cache, v_cache, q_stream, q_pos, window: int, n_sink: int = 0,
@@ -835,7 +844,7 @@ def msa_window_attn_prefill(shape: Shape, q, k_cache, v_cache, q_stream, q_pos, 
                             k_scale=None, v_scale=None):
     """msa_window_attn_decode for batches of many queries (prefill)."""
     return _ext_attn("msa_window_attn_prefill", MODE_PREFILL, shape, q, k_cache, v_cache, k_scale, v_scale, (),
-                     q_stream, q_pos, (window, n_sink), softmax_scale, out, workspace, stream, pages)
+                     q_stream, q_pos, _window(shape, window, n_sink), softmax_scale, out, workspace, stream, pages)
 
 
 def _append_step(shape: Shape, caches: dict, new: dict, b: dict, stream, pages, rope, indexer: bool):

@@ -472,7 +472,8 @@ typedef uint8_t msa_e4m3;
  *   scale grows, the call's rows are quantised with after (each to the nearest
  *   e4m3, ties to even; infinities become +-448, NaN stays NaN).
  * So the result does not depend on the order of the tokens in the call.
- * Other conditions as for msa_kv_append.  workspace: at least
+ * Other conditions as for msa_kv_append; two streams whose tables name one
+ * page must not both write it in a call (its scale would race).  workspace: at least
  * msa_kv_append_fp8_workspace_bytes(shape, n_tok) bytes, 16-byte aligned, its
  * contents need not be initialised (0 bytes, and NULL, for up to 256 tokens);
  * calls that may run at the same time on the GPU need separate workspaces. */

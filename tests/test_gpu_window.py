@@ -313,6 +313,22 @@ def test_memory_of_a_call_on_another_stream(form):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("f8", [False, True])
+def test_windows_past_32_bits(mode, f8):
+    """A window or a count of sinks larger than the capacity means the capacity, however large it is."""
+    S, G, cap, n = 1, 4, 384, 300
+    shape = msa.Shape(S, cap, 64, G)
+    gen = torch.Generator().manual_seed(9)
+    kv = make(S, G, cap, f8, gen)
+    q = torch.randn((n, 64, 128), generator=gen).bfloat16()
+    stream, pos = torch.zeros(n, dtype=torch.int32), (torch.arange(n) + cap - n).int()
+    for huge, same in (((2 ** 31 - 1, 0), (cap, 0)), ((2 ** 32, 0), (cap, 0)), ((2 ** 32 + 5, 2 ** 40), (cap, cap)),
+                       ((5, 2 ** 32), (5, cap))):
+        want = run(mode, shape, q, kv, stream, pos, *same, poison=False)
+        assert torch.equal(run(mode, shape, q, kv, stream, pos, *huge, poison=False), want)
+
+
 def test_large_offsets():
     """A pool of more than 2^31 bytes: pages beyond 32-bit byte offsets."""
     gen = torch.Generator().manual_seed(4)
@@ -412,5 +428,8 @@ def test_wrong_arguments_are_refused():
         for w, s in ((0, 0), (-3, 0), (4, -1)):
             with pytest.raises(msa.MsaError):
                 fn(shape, q, kv, kv, t, t, w, s)
+        for a in ((q, None, kv, t, t), (q, kv, None, t, t), (q, kv, kv, None, t), (q, kv, kv, t, None)):
+            with pytest.raises((ValueError, AttributeError)):
+                fn(shape, *a, 4)
     assert msa.msa_window_attn_decode(shape, q[:0], kv, kv, t[:0], t[:0], 4).shape == (0, 16, 128)
     PW.device_error()
