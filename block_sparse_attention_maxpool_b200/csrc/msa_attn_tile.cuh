@@ -407,8 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!seen) {
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                *reinterpret_cast<uint4*>(dst + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(dst + kHalf + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                const int at = row * 128 + (c ^ (lane & 7)) * 16;      // (eight lanes, eight bank groups)
+                *reinterpret_cast<uint4*>(dst + at) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(dst + kHalf + at) = make_uint4(0u, 0u, 0u, 0u);
               }
             }
           }
