@@ -106,7 +106,8 @@ struct Layout {
   static constexpr uint32_t kQOff = 0;                                   // A, B
   static constexpr uint32_t kKOff = 2 * kTile;
   static constexpr uint32_t kVOff = kKOff + kRing * kTile;
-  static constexpr uint32_t kRecOff = kVOff + kRing * kTile;
+  static constexpr uint32_t kOutOff = kVOff + kRing * kTile;             // 32 rows x 64 dims per softmax warp
+  static constexpr uint32_t kRecOff = kOutOff + 8 * 32 * 128;
   static constexpr uint32_t kBarOff = kRecOff + kRecs * sizeof(Rec);
   static constexpr uint32_t kEnd = kBarOff + 48 * 8;
   static constexpr size_t kBytes = kEnd + 1024;
@@ -709,20 +710,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const float inv = l != 0.f ? 1.f / l : 0.f;
+        // through shared memory, 64 dims at a time, so that a store covers whole
+        // 128-byte lines (a row per lane took 2 us more a task)
+        uint8_t* stage = smem + L::kOutOff + (warp - 4) * (32 * 128);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(obuf + c * 32, v);
-          tmem_ld_wait();
-          if (qi < P.n_q) {
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            float v[32];
+            tmem_ld32(obuf + half * 64 + c * 32, v);
+            tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 w = make_uint4(pack_bf16(v[i] * inv, v[i + 1] * inv), pack_bf16(v[i + 2] * inv, v[i + 3] * inv),
-                                   pack_bf16(v[i + 4] * inv, v[i + 5] * inv), pack_bf16(v[i + 6] * inv, v[i + 7] * inv));
+            for (int i = 0; i < 4; ++i) {
+              uint4 w = make_uint4(pack_bf16(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                   pack_bf16(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
               if (l == 0.f) w = make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4*>(dst + c * 32 + i) = w;
+              *reinterpret_cast<uint4*>(stage + swz128(lane, c * 4 + i)) = w;
             }
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i * 4 + (lane >> 3);        // row of the warp's 32
+            const int qr = q0 + x * 8 + quarter * 2 + rr / kHpg;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + swz128(rr, lane & 7));
+            if (qr < P.n_q)
+              *reinterpret_cast<uint4*>(P.out + (static_cast<size_t>(qr) * (P.G * kHpg) + g * kHpg + rr % kHpg) * kD + half * 64 +
+                                        (lane & 7) * 8) = w;
+          }
+          __syncwarp();
         }
         tc_fence_before();
         __syncwarp();
