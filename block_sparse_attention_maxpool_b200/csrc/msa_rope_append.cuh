@@ -453,11 +453,20 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_scale_kernel(const Fp8Params 
   }
 }
 
-// Quantise one row with its block's scale.
+// Quantise one row with its block's scale (a product where the scale is a
+// normal power of two, as this call makes them: its reciprocal is exact; a
+// caller's other scales are divided by).
 __device__ __forceinline__ void store_e4m3(uint8_t* row, const float (&a)[4], const float (&b)[4], int d0, int d1,
                                            float scale) {
-  *reinterpret_cast<uint32_t*>(row + d0) = to_e4m3x4(a[0] / scale, a[1] / scale, a[2] / scale, a[3] / scale);
-  *reinterpret_cast<uint32_t*>(row + d1) = to_e4m3x4(b[0] / scale, b[1] / scale, b[2] / scale, b[3] / scale);
+  const uint32_t e = __float_as_uint(scale);
+  if ((e & 0x807fffffu) == 0u && e - (1u << 23) < (252u << 23)) {
+    const float inv = __uint_as_float((254u << 23) - e);
+    *reinterpret_cast<uint32_t*>(row + d0) = to_e4m3x4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+    *reinterpret_cast<uint32_t*>(row + d1) = to_e4m3x4(b[0] * inv, b[1] * inv, b[2] * inv, b[3] * inv);
+  } else {
+    *reinterpret_cast<uint32_t*>(row + d0) = to_e4m3x4(a[0] / scale, a[1] / scale, a[2] / scale, a[3] / scale);
+    *reinterpret_cast<uint32_t*>(row + d1) = to_e4m3x4(b[0] / scale, b[1] / scale, b[2] / scale, b[3] / scale);
+  }
 }
 
 // 3 of 3: the call's rows.
