@@ -1104,16 +1104,16 @@ int make_map_8bit(CUtensorMap* m, const void* base, int64_t rows) {
 // on the device.  A call with fewer than four queries per stream on average
 // (and than one wave of work) takes the cluster kernel, a (query, group) per
 // cluster.  Measured on 148 SMs, cluster kernel against tiles (us): bf16, 4
-// groups, window 1024: 64 queries 32 / 49, 128 47 / 48, 512 127 / 51; window
-// 128: 128 28 / 34, 512 60 / 34; 32 streams of 16 queries 129 / 52.
+// groups, window 1024: 64 queries 33 / 43, 128 52 / 46, 512 132 / 47; window
+// 128: 128 31 / 31, 512 62 / 32; 32 streams of 16 queries 133 / 49, of 2 36 / 156.
 bool tiles_pay(const msa_shape* sh, int32_t n_q) {
   return static_cast<int64_t>(n_q) * sh->n_kv_heads >= 512 &&
          static_cast<int64_t>(n_q) >= int64_t{4} * std::min(sh->n_streams, n_q);
 }
 
 // Prefill calls over an 8-bit cache expand it to bf16 before they take the
-// tiles, which wants more queries: window 1024: 64 queries 34 / 66, 256 77 /
-// 66; window 4096: 64 67 / 124, 256 190 / 128, 1024 675 / 216.
+// tiles, which wants more queries: window 1024: 64 queries 37 / 67, 256 82 /
+// 67; window 4096: 64 71 / 121, 256 195 / 123, 1024 676 / 203.
 bool expands(const msa_shape* sh, int32_t n_q, int mode, bool f8) {
   return f8 && mode == MSA_MODE_PREFILL && static_cast<int64_t>(n_q) * sh->n_kv_heads >= 1024 &&
          static_cast<int64_t>(n_q) >= int64_t{16} * std::min(sh->n_streams, n_q);
