@@ -314,11 +314,25 @@ def msa_step_append(shape: Shape, idx_k_cache, k_cache, v_cache, idx_k_new, k_ne
           n, _stream(stream))
 
 
-def _workspace(shape: Shape, n: int, mode: int, workspace, device):
+def _held(t: torch.Tensor, stream) -> torch.Tensor:
+    """Tie memory allocated here (on the current stream) to the stream the call
+    launches on, so that it is not reused before that stream is done with it."""
+    if stream is not None and t.is_cuda:
+        raw, dev = _stream(stream), t.get_device()
+        t.record_stream(torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev))
+    return t
+
+
+def _empty(size: tuple, dtype, device, stream) -> torch.Tensor:
+    """A tensor for a call on ``stream``, which may outlive the caller's references to it."""
+    return _held(torch.empty(size, dtype=dtype, device=device), stream)
+
+
+def _workspace(shape: Shape, n: int, mode: int, workspace, device, stream):
     """(pointer, bytes) of the caller's workspace, allocating one if needed."""
     need = msa_workspace_bytes(shape, n, mode)
     if workspace is None and need > 0:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+        workspace = _empty((need,), torch.uint8, device, stream)
     if workspace is None:
         return 0, 0, None
     return _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel(), workspace
@@ -346,9 +360,8 @@ def msa_block_scores(shape: Shape, idx_q, idx_k_cache, q_stream, q_pos, block_sc
     else:
         fn, kdt = "msa_block_scores", torch.float32
     if block_scores is None:
-        block_scores = torch.empty((n, shape.n_kv_heads, shape.n_blocks), dtype=torch.float32,
-                                   device=idx_q.device)
-    ws_ptr, ws_bytes, _keep = _workspace(shape, n, MODE_DECODE, workspace, idx_q.device)
+        block_scores = _empty((n, shape.n_kv_heads, shape.n_blocks), torch.float32, idx_q.device, stream)
+    ws_ptr, ws_bytes, _keep = _workspace(shape, n, MODE_DECODE, workspace, idx_q.device, stream)
     _call(fn, shape, pages, _ptr(idx_q, torch.float32, (n, shape.n_kv_heads, shape.idx_dim), "idx_q"),
           _ptr(idx_k_cache, kdt, _cache_shape(shape, pages, shape.idx_dim), "idx_k_cache"),
           _ptr(q_stream, torch.int32, (n,), "q_stream"), _ptr(q_pos, torch.int32, (n,), "q_pos"), n,
@@ -361,9 +374,9 @@ def msa_select_topk(shape: Shape, block_scores, q_pos, sel=None, n_sel=None, str
     n = _n(q_pos, "q_pos")
     dev = block_scores.device
     if sel is None:
-        sel = torch.empty((n, shape.n_kv_heads, shape.top_k), dtype=torch.int32, device=dev)
+        sel = _empty((n, shape.n_kv_heads, shape.top_k), torch.int32, dev, stream)
     if n_sel is None:
-        n_sel = torch.empty((n, shape.n_kv_heads), dtype=torch.int32, device=dev)
+        n_sel = _empty((n, shape.n_kv_heads), torch.int32, dev, stream)
     s = shape.c()
     _check("msa_select_topk", library().msa_select_topk(
         ctypes.byref(s),
@@ -388,8 +401,8 @@ def _attn(fn_name: str, mode: int, shape: Shape, q, k_cache, v_cache, sel, q_str
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(shape.head_dim)
     if out is None:
-        out = torch.empty((n, shape.n_q_heads, shape.head_dim), dtype=torch.bfloat16, device=q.device)
-    ws_ptr, ws_bytes, _keep = _workspace(shape, n, mode, workspace, q.device)
+        out = _empty((n, shape.n_q_heads, shape.head_dim), torch.bfloat16, q.device, stream)
+    ws_ptr, ws_bytes, _keep = _workspace(shape, n, mode, workspace, q.device, stream)
     cs = _cache_shape(shape, pages, shape.head_dim)
     _call(fn_name, shape, pages, _ptr(q, torch.bfloat16, (n, shape.n_q_heads, shape.head_dim), "q"),
           _ptr(k_cache, torch.bfloat16, cs, "k_cache"), _ptr(v_cache, torch.bfloat16, cs, "v_cache"),
@@ -421,12 +434,12 @@ def msa_select_attn_decode(shape: Shape, block_scores, q, k_cache, v_cache, q_st
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(shape.head_dim)
     if sel is None:
-        sel = torch.empty((n, shape.n_kv_heads, shape.top_k), dtype=torch.int32, device=dev)
+        sel = _empty((n, shape.n_kv_heads, shape.top_k), torch.int32, dev, stream)
     if n_sel is None:
-        n_sel = torch.empty((n, shape.n_kv_heads), dtype=torch.int32, device=dev)
+        n_sel = _empty((n, shape.n_kv_heads), torch.int32, dev, stream)
     if out is None:
-        out = torch.empty((n, shape.n_q_heads, shape.head_dim), dtype=torch.bfloat16, device=dev)
-    ws_ptr, ws_bytes, _keep = _workspace(shape, n, MODE_DECODE, workspace, dev)
+        out = _empty((n, shape.n_q_heads, shape.head_dim), torch.bfloat16, dev, stream)
+    ws_ptr, ws_bytes, _keep = _workspace(shape, n, MODE_DECODE, workspace, dev, stream)
     cs = _cache_shape(shape, pages, shape.head_dim)
     _call("msa_select_attn_decode", shape, pages,
           _ptr(block_scores, torch.float32, (n, shape.n_kv_heads, shape.n_blocks), "block_scores"),
@@ -501,7 +514,7 @@ def msa_sparse_attn_decode_noalloc(shape: Shape, q, k_cache, v_cache, sel, q_str
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(shape.head_dim)
     if out is None:
-        out = torch.empty((n, shape.n_q_heads, shape.head_dim), dtype=torch.bfloat16, device=q.device)
+        out = _empty((n, shape.n_q_heads, shape.head_dim), torch.bfloat16, q.device, stream)
     cs = (shape.n_streams, shape.n_kv_heads, shape.capacity, shape.head_dim)
     s = shape.c()
     _check("msa_sparse_attn_decode_noalloc", library().msa_sparse_attn_decode_noalloc(
@@ -571,8 +584,7 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
     n = new["q_pos"].shape[0]
     mode = MODE_PREFILL if prefill else MODE_DECODE
     if b.get("workspace") is None and msa_workspace_bytes(shape, n, mode) > 0:
-        b = dict(b, workspace=torch.empty((msa_workspace_bytes(shape, n, mode),), dtype=torch.uint8,
-                                          device=new["q"].device))
+        b = dict(b, workspace=_empty((msa_workspace_bytes(shape, n, mode),), torch.uint8, new["q"].device, stream))
     bs = msa_block_scores(shape, new["idx_q"], caches["idx_k_cache"], new["q_stream"], new["q_pos"],
                           b.get("block_scores"), stream, b.get("workspace"), pages)
     if fp8:
@@ -616,15 +628,6 @@ def _on(dev: int, stream) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream)
-
-
-def _held(t: torch.Tensor, dev: int, stream) -> torch.Tensor:
-    """Tie memory allocated here (on the current stream) to the stream the call
-    launches on, so that it is not reused before that stream is done with it."""
-    if stream is not None:
-        raw = _stream(stream)
-        t.record_stream(torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev))
-    return t
 
 
 def _launch(fn: str, dev: int, args) -> None:
@@ -711,12 +714,12 @@ def msa_rope_append(shape: Shape, rope: Rope, k_cache=None, v_cache=None, k_new=
         qs = (nq, shape.n_q_heads, D)
         qi = _dptr(q, torch.bfloat16, qs, "q", dev)
         if q_out is None:
-            q_out = _held(torch.empty_like(q), dev, stream)
+            q_out = _held(torch.empty_like(q), stream)
         qo = _dptr(q_out, torch.bfloat16, qs, "q_out", dev)
     if idx_q is not None:
         iqi = _dptr(idx_q, torch.float32, (nq, G, Di), "idx_q", dev)
         if idx_q_out is None:
-            idx_q_out = _held(torch.empty_like(idx_q), dev, stream)
+            idx_q_out = _held(torch.empty_like(idx_q), stream)
         iqo = _dptr(idx_q_out, torch.float32, (nq, G, Di), "idx_q_out", dev)
     _launch("msa_rope_append", dev, (shape.c(), _pages_arg(shape, pages, dev), rope.c(dev), kc, vc, kn, vn, ic, f16,
                                      inew, ts, tp, nt, qi, qo, iqi, iqo, qp, nq, _on(dev, stream)))
@@ -743,7 +746,7 @@ def msa_kv_append_fp8(shape: Shape, k_cache, v_cache, k_scale, v_scale, k_new, v
     need = 0
     if workspace is None:
         need = msa_kv_append_fp8_workspace_bytes(shape, n)
-        workspace = _held(torch.empty((need,), dtype=torch.uint8, device=dev), dev, stream) if need > 0 else None
+        workspace = _empty((need,), torch.uint8, dev, stream) if need > 0 else None
     _launch("msa_kv_append_fp8", dev, (
         shape.c(), _pages_arg(shape, pages, dev), None if rope is None else rope.c(dev),
         _dptr(k_cache, torch.float8_e4m3fn, cs, "k_cache", dev), _dptr(v_cache, torch.float8_e4m3fn, cs, "v_cache", dev),
@@ -770,7 +773,7 @@ def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_
     qs = (n, shape.n_q_heads, shape.head_dim)
     qp = _dptr(q, torch.bfloat16, qs, "q", dev)
     if out is None:
-        out = _held(torch.empty_like(q), dev, stream)
+        out = _held(torch.empty_like(q), stream)
     cs = _cache_shape(shape, pages, shape.head_dim)
     if k_cache.dtype is torch.float8_e4m3fn:
         if k_scale is None or v_scale is None:
@@ -788,7 +791,7 @@ def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_
     if workspace is None and mode == MODE_PREFILL and k_scale is not None:
         need = msa_attn_workspace_bytes(shape, n, mode, True, pages)
         if need > 0:
-            workspace = _held(torch.empty((need,), dtype=torch.uint8, device=dev), dev, stream)
+            workspace = _empty((need,), torch.uint8, dev, stream)
     if workspace is not None:
         wp, wb = _dptr(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel()
     if softmax_scale is None:
@@ -924,7 +927,7 @@ def msa_dsa_token_scores(shape: DsaShape, q_idx, weights, k_idx_cache, q_stream,
     """Lightning-indexer scores [n_q][capacity] (float32, -inf past each query)."""
     n = _n(q_pos, "q_pos")
     if scores is None:
-        scores = torch.empty((n, shape.capacity), dtype=torch.float32, device=q_idx.device)
+        scores = _empty((n, shape.capacity), torch.float32, q_idx.device, stream)
     s = shape.c()
     _check("msa_dsa_token_scores", library().msa_dsa_token_scores(
         ctypes.byref(s), _dsa_pages(_as_msa_shape(shape), pages),
@@ -941,9 +944,9 @@ def msa_dsa_select_topk(shape: DsaShape, scores, q_pos, sel=None, n_sel=None, st
     n = _n(q_pos, "q_pos")
     dev = scores.device
     if sel is None:
-        sel = torch.empty((n, DSA_SEL_WIDTH), dtype=torch.int32, device=dev)
+        sel = _empty((n, DSA_SEL_WIDTH), torch.int32, dev, stream)
     if n_sel is None:
-        n_sel = torch.empty((n,), dtype=torch.int32, device=dev)
+        n_sel = _empty((n,), torch.int32, dev, stream)
     s = shape.c()
     _check("msa_dsa_select_topk", library().msa_dsa_select_topk(
         ctypes.byref(s), _ptr(scores, torch.float32, (n, shape.capacity), "scores"),
@@ -959,8 +962,8 @@ def msa_dsa_sparse_attn_decode(shape: Shape, q, k_cache, v_cache, sel, q_stream,
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(shape.head_dim)
     if out is None:
-        out = torch.empty((n, shape.n_q_heads, shape.head_dim), dtype=torch.bfloat16, device=q.device)
-    ws_ptr, ws_bytes, _keep = _workspace(shape, n, MODE_DECODE, workspace, q.device)
+        out = _empty((n, shape.n_q_heads, shape.head_dim), torch.bfloat16, q.device, stream)
+    ws_ptr, ws_bytes, _keep = _workspace(shape, n, MODE_DECODE, workspace, q.device, stream)
     cs = _cache_shape(shape, pages, shape.head_dim)
     s = shape.c()
     _check("msa_dsa_sparse_attn_decode", library().msa_dsa_sparse_attn_decode(
@@ -1019,20 +1022,20 @@ def msa_decode_step_fused(shape: Shape, caches: dict, new: dict, bufs: dict | No
         softmax_scale = 1.0 / math.sqrt(shape.head_dim)
     bs = b.get("block_scores")
     if bs is None:
-        bs = torch.empty((n, G, shape.n_blocks), dtype=torch.float32, device=dev)
+        bs = _empty((n, G, shape.n_blocks), torch.float32, dev, stream)
     sel = b.get("sel")
     if sel is None:
-        sel = torch.empty((n, G, shape.top_k), dtype=torch.int32, device=dev)
+        sel = _empty((n, G, shape.top_k), torch.int32, dev, stream)
     n_sel = b.get("n_sel")
     if n_sel is None:
-        n_sel = torch.empty((n, G), dtype=torch.int32, device=dev)
+        n_sel = _empty((n, G), torch.int32, dev, stream)
     out = b.get("out")
     if out is None:
-        out = torch.empty((n, shape.n_q_heads, shape.head_dim), dtype=torch.bfloat16, device=dev)
+        out = _empty((n, shape.n_q_heads, shape.head_dim), torch.bfloat16, dev, stream)
     ws = b.get("workspace_fused")
     need = msa_decode_step_fused_workspace_bytes(shape, n) if n > 0 else 0
     if ws is None and need > 0:
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+        ws = _empty((need,), torch.uint8, dev, stream)
     cs = (shape.n_streams, G, shape.capacity)
     s = shape.c()
     _check("msa_decode_step_fused", library().msa_decode_step_fused(
