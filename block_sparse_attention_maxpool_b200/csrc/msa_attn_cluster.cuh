@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, Unit<kF8>::kCtas)
           } else {
             row = static_cast<int>(blk) + first % kBlock;   // the host checks that every row fits 31 bits
             if (kF8) {
-              ks = __ldg(P.k_scale + blk / kBlock);
-              vs = __ldg(P.v_scale + blk / kBlock);
+              ks = __ldcg(P.k_scale + blk / kBlock);      // (the append before may have written them)
+              vs = __ldcg(P.v_scale + blk / kBlock);
             }
           }
         }

@@ -155,7 +155,7 @@ __device__ __forceinline__ bool tok_unit(const Params& P, long long u, int& s, i
     return false;
   }
   toks = P.tok_sel + static_cast<size_t>(qi) * (kTopK * kBlock) + j * kBlock;
-  return __ldg(toks) >= 0;
+  return __ldcg(toks) >= 0;
 }
 
 // Cache row of a selected token, or -1 when the slot is padding, names a
@@ -498,7 +498,7 @@ __device__ __forceinline__ void sparse_attn_decode_sk_body(const CUtensorMap* tm
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = pw * 64 + lane + 32 * i;
-          const int tok = __ldg(toks + r);
+          const int tok = __ldcg(toks + r);
           const long long row = tok_row(P, s, g, p, tok);
           if (row < 0 && tok >= 0) raise_error(tok > p ? MSA_DEVERR_SEL_RANGE : MSA_DEVERR_PAGE_RANGE);
           m[i] = __ballot_sync(0xffffffffu, row >= 0);

@@ -295,7 +295,7 @@ __device__ __forceinline__ void build_plan(const Params& P, int t, Plan& pl, int
   {
     int4 sel4 = make_int4(-1, -1, -1, -1);
     if (qpos >= 0)
-      sel4 = __ldg(reinterpret_cast<const int4*>(P.sel + (static_cast<size_t>(q0 + q) * P.G + g) * kTopK) + (lane & 3));
+      sel4 = __ldcg(reinterpret_cast<const int4*>(P.sel + (static_cast<size_t>(q0 + q) * P.G + g) * kTopK) + (lane & 3));
     const int b4[4] = {sel4.x, sel4.y, sel4.z, sel4.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

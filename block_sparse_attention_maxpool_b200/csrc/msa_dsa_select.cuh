@@ -87,9 +87,9 @@ struct SmemKeys {
 // of 128 floats, 16-byte aligned).
 struct RowKeys {
   const float* row;
-  __device__ __forceinline__ uint32_t operator()(int i) const { return score_key(__ldg(row + i)); }
+  __device__ __forceinline__ uint32_t operator()(int i) const { return score_key(__ldcg(row + i)); }
   __device__ __forceinline__ uint4 get4(int i) const {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(row + i));
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(row + i));
     return make_uint4(score_key(v.x), score_key(v.y), score_key(v.z), score_key(v.w));
   }
 };
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   int need;
   if constexpr (kStaged) {
 #pragma unroll 8
-    for (int i = tid; i < n; i += kSelThreads) sm.keys[i] = score_key(__ldg(row + i));   // loads in flight
+    for (int i = tid; i < n; i += kSelThreads) sm.keys[i] = score_key(__ldcg(row + i));   // loads in flight
     __syncthreads();
     const SmemKeys get{sm.keys};
     if (n < kSampleMin || !sample_kth(sm, get, n, top_k, &T, &need)) radix_kth(sm, get, n, top_k, &T, &need);
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   const int m = hi - lo;
   const float* row = scores + static_cast<size_t>(t) * capacity + lo;
 #pragma unroll 8
-  for (int i = tid; i < m; i += kSelThreads) sm.keys[i] = score_key(__ldg(row + i));
+  for (int i = tid; i < m; i += kSelThreads) sm.keys[i] = score_key(__ldcg(row + i));
   for (int i = m + tid; i < ((m + 3) & ~3); i += kSelThreads) sm.keys[i] = 0u;   // whole vectors for get4
   if (rank == 0) {
     for (int b = tid; b < 256; b += kSelThreads) sm.chist[b] = 0;

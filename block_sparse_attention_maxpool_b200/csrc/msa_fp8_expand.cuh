@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(256) expand_kernel(const Params P) {
     const int b = i < sinks ? i : win + i - sinks;
     const long long row = kv_block_row(P.pages, s, g, b, P.G, P.capacity);
     if (row < 0) continue;                       // the attention kernel reports it
-    const float ks = P.k_scale[row / 128], vs = P.v_scale[row / 128];
+    const float ks = __ldcg(P.k_scale + row / 128), vs = __ldcg(P.v_scale + row / 128);
     const uint4* k = reinterpret_cast<const uint4*>(P.k_cache + row * 128);
     const uint4* v = reinterpret_cast<const uint4*>(P.v_cache + row * 128);
     uint4* ko = P.k_out + row * 16;
@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(256) expand_kernel(const Params P) {
     uint4 x[4], y[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      x[c] = __ldg(k + threadIdx.x + 256 * c);
-      y[c] = __ldg(v + threadIdx.x + 256 * c);
+      x[c] = __ldcs(k + threadIdx.x + 256 * c);
+      y[c] = __ldcs(v + threadIdx.x + 256 * c);
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {

@@ -256,10 +256,10 @@ __device__ __forceinline__ void block_scores_gemv_body(const Params<KeyT>& P, ui
       cur_qg = qg;
       const float4* qp = reinterpret_cast<const float4*>(P.idx_q + static_cast<size_t>(qg) * kDi);
       if constexpr (kF16) {   // dims 8j .. 8j+7, j = lane_in_row
-        qv = __ldg(qp + 2 * lane_in_row);
-        qv2 = __ldg(qp + 2 * lane_in_row + 1);
+        qv = __ldcg(qp + 2 * lane_in_row);
+        qv2 = __ldcg(qp + 2 * lane_in_row + 1);
       } else {                // dims 4 * lane .. +3
-        qv = __ldg(qp + lane_in_row);
+        qv = __ldcg(qp + lane_in_row);
       }
     }
     float m = -INFINITY;

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(256) tc_split_queries_kernel(const Params P) {
   const bool real = q < P.n_q;
   const bool ok = real && query_ok(P, q, s, p);
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (real) x = __ldg(reinterpret_cast<const float4*>(P.idx_q + (static_cast<size_t>(q) * P.G + g) * kDi) + lane);
+  if (real) x = __ldcs(reinterpret_cast<const float4*>(P.idx_q + (static_cast<size_t>(q) * P.G + g) * kDi) + lane);
   __half2 hi[2], lo[2];
   const int e = split_row4(x, hi, lo);
   const size_t row = static_cast<size_t>(g) * P.n_q_pad + q;
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 4; ++c) {
 #pragma unroll
             for (int i4 = 0; i4 < 8; ++i4) {
-              const float4 k4 = __ldg(ksc + c * 8 + i4);
+              const float4 k4 = ksc[c * 8 + i4];
               const float2 x01 = fmul2(make_float2(v[c][i4 * 4], v[c][i4 * 4 + 1]), make_float2(k4.x, k4.y));
               const float2 x23 = fmul2(make_float2(v[c][i4 * 4 + 2], v[c][i4 * 4 + 3]), make_float2(k4.z, k4.w));
               float x[4] = {x01.x, x01.y, x23.x, x23.y};
