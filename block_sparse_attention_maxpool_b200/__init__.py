@@ -882,13 +882,19 @@ def window_step(shape: Shape, caches: dict, new: dict, window: int, n_sink: int 
 
     caches: k_cache, v_cache (bfloat16, or float8_e4m3fn with k_scale and
     v_scale); new: tok_stream, tok_pos, k_new, v_new, q_stream, q_pos, q.
-    ``bufs`` may hold preallocated out / q_rot / workspace_fp8 / workspace.
+    ``bufs`` may hold preallocated out / q_rot / workspace_fp8 / workspace_attn,
+    as for decode_step (whose bufs serve here too), or ``workspace`` for the
+    attention, used when it is large enough.
     With ``rope`` keys and queries arrive unrotated.  Returns out."""
     b = bufs or {}
     q, _ = _append_step(shape, caches, new, b, stream, pages, rope, False)
     attend = msa_window_attn_prefill if prefill else msa_window_attn_decode
+    ws = b.get("workspace_attn")
+    if ws is None and b.get("workspace") is not None and prefill and caches.get("k_scale") is not None:
+        if b["workspace"].numel() >= msa_attn_workspace_bytes(shape, new["q_pos"].shape[0], MODE_PREFILL, True, pages):
+            ws = b["workspace"]
     return attend(shape, q, caches["k_cache"], caches["v_cache"], new["q_stream"], new["q_pos"], window, n_sink, None,
-                  b.get("out"), b.get("workspace"), stream, pages, caches.get("k_scale"), caches.get("v_scale"))
+                  b.get("out"), ws, stream, pages, caches.get("k_scale"), caches.get("v_scale"))
 
 
 # ---- token-level variant (lightning indexer) --------------------------------

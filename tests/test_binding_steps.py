@@ -1,0 +1,62 @@
+"""How the binding's step functions pass their arguments on (no GPU: the calls below them are stand-ins), and the same
+steps on the GPU."""
+import pytest
+import torch
+
+import block_sparse_attention_maxpool_b200 as msa
+from block_sparse_attention_maxpool_b200 import build as msa_build
+
+F8 = torch.float8_e4m3fn
+SHAPE = msa.Shape(2, 1024)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    msa_build.build()
+
+
+def step_inputs(n):
+    i = torch.zeros(n, dtype=torch.int32)
+    return dict(tok_stream=i, tok_pos=i, q_stream=i, q_pos=i, k_new=None, v_new=None, q=torch.zeros(1))
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("f8", [False, True])
+def test_window_step_takes_the_bufs_of_decode_step(monkeypatch, prefill, f8):
+    """One bufs dict for the layers of a model: ``workspace`` is the scoring workspace there, often too small for the
+    attention of an 8-bit prompt."""
+    n = 300
+    need = msa.msa_attn_workspace_bytes(SHAPE, n, msa.MODE_PREFILL if prefill else msa.MODE_DECODE, f8)
+    seen = []
+    monkeypatch.setattr(msa, "_append_step", lambda *a: (None, None))
+    for name in ("msa_window_attn_prefill", "msa_window_attn_decode"):
+        monkeypatch.setattr(msa, name, lambda *a: seen.append(a[10]))
+    caches = dict(k_cache=torch.zeros(1).to(F8 if f8 else torch.bfloat16), v_cache=None)
+    if f8:
+        caches.update(k_scale=1, v_scale=1)
+    small, large, own = (torch.zeros(m, dtype=torch.uint8) for m in (64, need + 64, need + 32))
+    for bufs in ({"workspace": small}, {"workspace": small, "workspace_attn": own}, {"workspace": large}, {}, None):
+        msa.window_step(SHAPE, caches, step_inputs(n), 100, 4, bufs, prefill=prefill)
+    assert seen[0] is None or need <= 64 and seen[0] is small
+    assert seen[1] is own
+    assert seen[2] is (large if f8 and prefill else None)
+    assert seen[3] is None and seen[4] is None
+
+
+@pytest.mark.gpu
+def test_one_bufs_for_both_kinds_of_layers():
+    """A selection layer and a window layer of one model share their bufs over an 8-bit prompt."""
+    shape, n = msa.Shape(1, 1024), 300
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    randn = lambda *d, t=torch.bfloat16: torch.randn(d, device="cuda", generator=gen).to(t)
+    at = dict(stream=torch.zeros(n, dtype=torch.int32, device="cuda"), pos=torch.arange(n, dtype=torch.int32, device="cuda"))
+    new = dict(tok_stream=at["stream"], tok_pos=at["pos"], q_stream=at["stream"], q_pos=at["pos"], k_new=randn(n, 4, 128),
+               v_new=randn(n, 4, 128), q=randn(n, 64, 128), idx_k_new=randn(n, 4, 128, t=torch.float32),
+               idx_q=randn(n, 4, 128, t=torch.float32))
+    bufs = {"workspace": torch.zeros(msa.msa_workspace_bytes(shape, n, msa.MODE_PREFILL), dtype=torch.uint8, device="cuda")}
+    out = []
+    for b in (None, bufs):
+        c = dict(msa.fp8_caches(shape, "cuda"), idx_k_cache=torch.zeros((1, 4, 1024, 128), device="cuda"))
+        out.append((msa.decode_step(shape, c, new, b, prefill=True)[0], msa.window_step(shape, c, new, 100, 4, b, prefill=True)))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert msa.msa_get_device_error() == 0
