@@ -73,11 +73,15 @@ class Shape:
         return self.capacity // self.block
 
     def c(self) -> CShape:
+        return CShape(self.n_streams, self.capacity, self.n_q_heads, self.n_kv_heads,
+                      self.head_dim, self.idx_dim, self.block, self.top_k)
+
+    def _shared(self) -> CShape:
+        """c(), made once: for the library, which only reads it."""
         c = self.__dict__.get("_c")
         if c is None:
-            c = CShape(self.n_streams, self.capacity, self.n_q_heads, self.n_kv_heads,
-                       self.head_dim, self.idx_dim, self.block, self.top_k)
-            object.__setattr__(self, "_c", c)          # the library only reads it
+            c = self.c()
+            object.__setattr__(self, "_c", c)
         return c
 
 
@@ -721,13 +725,13 @@ def msa_rope_append(shape: Shape, rope: Rope, k_cache=None, v_cache=None, k_new=
         if idx_q_out is None:
             idx_q_out = _held(torch.empty_like(idx_q), stream)
         iqo = _dptr(idx_q_out, torch.float32, (nq, G, Di), "idx_q_out", dev)
-    _launch("msa_rope_append", dev, (shape.c(), _pages_arg(shape, pages, dev), rope.c(dev), kc, vc, kn, vn, ic, f16,
+    _launch("msa_rope_append", dev, (shape._shared(), _pages_arg(shape, pages, dev), rope.c(dev), kc, vc, kn, vn, ic, f16,
                                      inew, ts, tp, nt, qi, qo, iqi, iqo, qp, nq, _on(dev, stream)))
     return q_out, idx_q_out
 
 
 def msa_kv_append_fp8_workspace_bytes(shape: Shape, n_tok: int) -> int:
-    v = library().msa_kv_append_fp8_workspace_bytes(shape.c(), n_tok)
+    v = library().msa_kv_append_fp8_workspace_bytes(shape._shared(), n_tok)
     if v == ctypes.c_size_t(-1).value:
         raise MsaError("msa_kv_append_fp8_workspace_bytes", -3)
     return v
@@ -748,7 +752,7 @@ def msa_kv_append_fp8(shape: Shape, k_cache, v_cache, k_scale, v_scale, k_new, v
         need = msa_kv_append_fp8_workspace_bytes(shape, n)
         workspace = _empty((need,), torch.uint8, dev, stream) if need > 0 else None
     _launch("msa_kv_append_fp8", dev, (
-        shape.c(), _pages_arg(shape, pages, dev), None if rope is None else rope.c(dev),
+        shape._shared(), _pages_arg(shape, pages, dev), None if rope is None else rope.c(dev),
         _dptr(k_cache, torch.float8_e4m3fn, cs, "k_cache", dev), _dptr(v_cache, torch.float8_e4m3fn, cs, "v_cache", dev),
         _dptr(k_scale, torch.float32, ss, "k_scale", dev), _dptr(v_scale, torch.float32, ss, "v_scale", dev),
         _dptr(k_new, torch.bfloat16, ns, "k_new", dev), _dptr(v_new, torch.bfloat16, ns, "v_new", dev),
@@ -760,7 +764,7 @@ def msa_kv_append_fp8(shape: Shape, k_cache, v_cache, k_scale, v_scale, k_new, v
 def msa_attn_workspace_bytes(shape: Shape, n_q: int, mode: int, fp8: bool = False, pages: Pages | None = None) -> int:
     """Workspace of the window and 8-bit attention calls (0 but for prefill over an 8-bit cache)."""
     pg = None if pages is None else CPages(0, pages.n_pages)
-    v = library().msa_attn_workspace_bytes(shape.c(), pg, n_q, mode, int(fp8))
+    v = library().msa_attn_workspace_bytes(shape._shared(), pg, n_q, mode, int(fp8))
     if v == ctypes.c_size_t(-1).value:
         raise MsaError("msa_attn_workspace_bytes", -3)
     return v
@@ -796,7 +800,7 @@ def _ext_attn(fn: str, mode: int, shape: Shape, q, k_cache, v_cache, k_scale, v_
         wp, wb = _dptr(workspace, torch.uint8, workspace.shape, "workspace", dev), workspace.numel()
     if softmax_scale is None:
         softmax_scale = shape.head_dim ** -0.5
-    _launch(fn, dev, (shape.c(), _pages_arg(shape, pages, dev), qp, *kv, *extra,
+    _launch(fn, dev, (shape._shared(), _pages_arg(shape, pages, dev), qp, *kv, *extra,
                       _dptr(q_stream, torch.int32, (n,), "q_stream", dev), _dptr(q_pos, torch.int32, (n,), "q_pos", dev),
                       n, *tail, softmax_scale, _dptr(out, torch.bfloat16, qs, "out", dev), wp, wb, _on(dev, stream)))
     return out

@@ -1,5 +1,8 @@
 """How the binding's step functions pass their arguments on (no GPU: the calls below them are stand-ins), and the same
 steps on the GPU."""
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -13,6 +16,18 @@ SHAPE = msa.Shape(2, 1024)
 @pytest.fixture(scope="module", autouse=True)
 def _lib():
     msa_build.build()
+
+
+def test_shape_hands_out_its_own_copy():
+    """What a caller does to the C structure does not reach the frozen Shape, nor what the library gets of it."""
+    shape = msa.Shape(2, 1024, 64, 4)
+    want = msa.msa_attn_workspace_bytes(shape, 400, msa.MODE_PREFILL, True)
+    c = shape.c()
+    c.capacity, c.n_streams = 128, 1
+    assert (shape.c().capacity, shape.c().n_streams) == (1024, 2)
+    assert msa.msa_attn_workspace_bytes(shape, 400, msa.MODE_PREFILL, True) == want
+    for twin in (copy.copy(shape), copy.deepcopy(shape), pickle.loads(pickle.dumps(shape))):
+        assert twin == shape and msa.msa_attn_workspace_bytes(twin, 400, msa.MODE_PREFILL, True) == want
 
 
 def step_inputs(n):
