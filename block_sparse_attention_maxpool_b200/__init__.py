@@ -555,6 +555,11 @@ def msa_version() -> int:
     return library().msa_version()
 
 
+def _elsewhere(t: torch.Tensor) -> bool:
+    """A tensor on another CUDA device than the current one."""
+    return t.is_cuda and t.get_device() != torch._C._cuda_getDevice()
+
+
 def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None, stream=None,
                 prefill: bool = False, pages: Pages | None = None, rope: Rope | None = None):
     """One MSA step through the C ABI: append the new tokens' indexer keys
@@ -572,6 +577,9 @@ def decode_step(shape: Shape, caches: dict, new: dict, bufs: dict | None = None,
     attention).
     Returns (out, sel, n_sel, block_scores).
     """
+    if _elsewhere(new["q"]):                # launch all of the step's calls on its tensors' device
+        with torch.cuda.device(new["q"].device):
+            return decode_step(shape, caches, new, bufs, stream, prefill, pages, rope)
     b = bufs or {}
     fp8 = caches["k_cache"].dtype is torch.float8_e4m3fn
     if rope is not None or fp8:
@@ -890,6 +898,9 @@ def window_step(shape: Shape, caches: dict, new: dict, window: int, n_sink: int 
     as for decode_step (whose bufs serve here too), or ``workspace`` for the
     attention, used when it is large enough.
     With ``rope`` keys and queries arrive unrotated.  Returns out."""
+    if _elsewhere(new["q"]):
+        with torch.cuda.device(new["q"].device):
+            return window_step(shape, caches, new, window, n_sink, bufs, stream, prefill, pages, rope)
     b = bufs or {}
     q, _ = _append_step(shape, caches, new, b, stream, pages, rope, False)
     attend = msa_window_attn_prefill if prefill else msa_window_attn_decode

@@ -58,6 +58,52 @@ def test_window_step_takes_the_bufs_of_decode_step(monkeypatch, prefill, f8):
     assert seen[3] is None and seen[4] is None
 
 
+class _OnDevice1:
+    """Stands for a tensor on cuda:1."""
+    is_cuda, device, dtype, shape = True, torch.device("cuda", 1), torch.bfloat16, (1,)
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("step", ["decode_step", "window_step"])
+def test_steps_launch_on_the_device_of_their_tensors(monkeypatch, step, prefill, f8):
+    """With another device current, every call of a step runs with the tensors' device current, and the old one is
+    current again afterwards."""
+    current, seen = [0], []
+
+    class use:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *a):
+            current[0] = self.before
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", use)
+
+    def stand_in(result):
+        return lambda *a, **k: (seen.append(current[0]), result)[1]
+    for name in ("msa_kv_append", "msa_step_append", "msa_block_scores", "msa_kv_append_fp8", "msa_indexer_append",
+                 "msa_sparse_attn_prefill", "msa_sparse_attn_prefill_fp8", "msa_sparse_attn_decode_fp8",
+                 "msa_window_attn_decode", "msa_window_attn_prefill"):
+        monkeypatch.setattr(msa, name, stand_in(None))
+    monkeypatch.setattr(msa, "msa_select_topk", stand_in((None, None)))
+    monkeypatch.setattr(msa, "msa_select_attn_decode", stand_in((None, None, None)))
+    monkeypatch.setattr(msa, "msa_workspace_bytes", lambda *a: 0)
+    new = dict(step_inputs(3), q=_OnDevice1(), idx_q=None, idx_k_new=None)
+    caches = dict(k_cache=torch.zeros(1).to(F8 if f8 else torch.bfloat16), v_cache=None, idx_k_cache=torch.zeros(1))
+    if f8:
+        caches.update(k_scale=1, v_scale=1)
+    args = (100, 4) if step == "window_step" else ()
+    getattr(msa, step)(SHAPE, caches, new, *args, prefill=prefill)
+    assert len(seen) >= 2 and set(seen) == {1} and current == [0]
+
+
 @pytest.mark.gpu
 def test_one_bufs_for_both_kinds_of_layers():
     """A selection layer and a window layer of one model share their bufs over an 8-bit prompt."""
