@@ -1262,18 +1262,22 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   msa::KvPages pg;
   int64_t rows = 0;
   if ((st = pages_of(sh, pages, &pg, &rows)) != MSA_OK) return st;
-  const size_t need = ext_attn_workspace(sh, rows, n_q, mode, a.f8);
+  size_t need = ext_attn_workspace(sh, rows, n_q, mode, a.f8);
+  int sms = 0;
+  // a selection that does not take the tiles needs no workspace (the selection tiles take a positive scale)
+  if (!win && need > 0) {
+    if ((st = current_device_sms(&sms)) != MSA_OK) return st;
+    if (!(softmax_scale > 0.f) || !selection_tiles_pay(sh, n_q, sms)) need = 0;
+  }
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return MSA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MSA_ERR_ALIGN;
   }
-  int sms = 0;
-  if ((st = current_device_sms(&sms)) != MSA_OK) return st;
+  if (sms == 0 && (st = current_device_sms(&sms)) != MSA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int window = std::min(a.window, sh->capacity);
   const int n_sink = std::min(a.n_sink, sh->capacity);
-  // (the selection tiles take a positive scale)
-  if (need > 0 && (win || (softmax_scale > 0.f && selection_tiles_pay(sh, n_q, sms)))) {
+  if (need > 0) {
     const ExpandLayout l = expand_layout(sh, rows, n_q);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     msa::expand::Params E;
