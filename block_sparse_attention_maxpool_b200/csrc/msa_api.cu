@@ -212,7 +212,8 @@ int sparse_attn(const msa_shape* sh, const msa_bf16* q, const msa_bf16* k_cache,
                 const int32_t* sel, const int32_t* q_stream, const int32_t* q_pos, int32_t n_q,
                 float softmax_scale, msa_bf16* out, void* workspace, size_t workspace_bytes, void* stream,
                 int mode, const msa_pages* pages, const int32_t* tok_sel = nullptr,
-                const float* block_scores = nullptr, int32_t* sel_out = nullptr, int32_t* n_sel_out = nullptr) {
+                const float* block_scores = nullptr, int32_t* sel_out = nullptr, int32_t* n_sel_out = nullptr,
+                msa::Gate gate = {}) {
   int st = check_shape(sh);
   if (st != MSA_OK) return st;
   if (n_q < 0) return MSA_ERR_RANGE;
@@ -263,6 +264,7 @@ int sparse_attn(const msa_shape* sh, const msa_bf16* q, const msa_bf16* k_cache,
     U.n_tiles = (n_q + msa::uattn::kTileQ - 1) / msa::uattn::kTileQ;
     U.scale_log2 = softmax_scale * 1.4426950408889634f;
     U.pages = pg;
+    U.gate = gate;
     U.plans = static_cast<msa::uattn::Plan*>(workspace);
     const int64_t tasks = static_cast<int64_t>(G) * U.n_tiles;
     const int64_t ugrid = std::min<int64_t>(sms, tasks);
@@ -1132,19 +1134,36 @@ bool selection_tiles_pay(const msa_shape* sh, int32_t n_q, int sms) {
   return 70.0 + waves * apart < 10.0 + 0.085 * (148.0 / sms) * pairs * std::min(nblk, 16.0) / 16.0;
 }
 
+// An expanded cache or pool larger than this goes into pages of the call's own,
+// as many as fit here: 2^21 slots of one group, 512K tokens of four.  (As large
+// as the cache, the workspace of a serving-size pool would be twice the pool.)
+constexpr int64_t kExpandBytes = int64_t{1} << 30;
+constexpr int64_t kExpandRow = 2 * 128 * sizeof(msa_bf16);       // K and V of a slot
+
 struct ExpandLayout {
-  size_t range, plans, k, v, total;
+  int64_t room;               // pages of the call's own; 0: laid out as the cache
+  int64_t rows;               // of the expanded K and V
+  size_t control, base, table, plans, k, v, total;
 };
 
 // rows: of the cache or page pool.
 ExpandLayout expand_layout(const msa_shape* sh, int64_t rows, int32_t n_q) {
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const int64_t blocks = static_cast<int64_t>(sh->n_streams) * (sh->capacity / 128);
   ExpandLayout l;
-  l.range = 0;
-  l.plans = up(static_cast<size_t>(sh->n_streams) * 2 * sizeof(int32_t));
+  l.room = 0;
+  l.rows = rows;
+  if (rows * kExpandRow > kExpandBytes) {
+    l.room = std::min(blocks, std::max<int64_t>(1, kExpandBytes / (kExpandRow * 128 * sh->n_kv_heads)));
+    l.rows = l.room * sh->n_kv_heads * 128;
+  }
+  l.control = up((4 + static_cast<size_t>(sh->n_streams) * 2) * sizeof(int32_t));
+  l.base = l.control;
+  l.table = up(l.base + (l.room > 0 ? sh->n_streams : 0) * sizeof(int32_t));
+  l.plans = up(l.table + (l.room > 0 ? blocks : 0) * sizeof(int32_t));
   l.k = up(l.plans + attn_workspace(sh, n_q, MSA_MODE_PREFILL));
-  l.v = l.k + static_cast<size_t>(rows) * 128 * sizeof(msa_bf16);
-  l.total = l.v + static_cast<size_t>(rows) * 128 * sizeof(msa_bf16);
+  l.v = l.k + static_cast<size_t>(l.rows) * 128 * sizeof(msa_bf16);
+  l.total = l.v + static_cast<size_t>(l.rows) * 128 * sizeof(msa_bf16);
   return l;
 }
 
@@ -1213,7 +1232,7 @@ int launch_cluster_attn(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const 
 
 int tile_attn(const msa_shape* sh, const msa_bf16* q, const void* k, const void* v, const msa::KvPages& pg, int64_t rows,
               const int32_t* q_stream, const int32_t* q_pos, int32_t n_q, int window, int n_sink, float softmax_scale,
-              msa_bf16* out, int sms, cudaStream_t s) {
+              msa_bf16* out, int sms, msa::Gate gate, cudaStream_t s) {
   CUtensorMap tm_q, tm_k, tm_v;
   int st;
   if ((st = make_kv_map(&tm_k, k, rows)) != MSA_OK) return st;
@@ -1236,6 +1255,7 @@ int tile_attn(const msa_shape* sh, const msa_bf16* q, const void* k, const void*
   T.n_sink = n_sink;
   T.scale_log2 = softmax_scale * 1.4426950408889634f;
   T.pages = pg;
+  T.gate = gate;
   const int64_t tasks = static_cast<int64_t>(T.G) * T.n_tiles;
   return cuda_status(launch(msa::tattn::attn_tile_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(sms, tasks))),
                             dim3(msa::tattn::kThreads), msa::tattn::Layout::kBytes, s, tm_q, tm_k, tm_v, T));
@@ -1277,6 +1297,7 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int window = std::min(a.window, sh->capacity);
   const int n_sink = std::min(a.n_sink, sh->capacity);
+  msa::Gate cluster_gate;
   if (need > 0) {
     const ExpandLayout l = expand_layout(sh, rows, n_q);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1287,7 +1308,11 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     E.v_scale = a.v_scale;
     E.k_out = reinterpret_cast<uint4*>(ws + l.k);
     E.v_out = reinterpret_cast<uint4*>(ws + l.v);
-    E.range = reinterpret_cast<int32_t*>(ws + l.range);
+    E.ctl = reinterpret_cast<int32_t*>(ws);
+    E.range = E.ctl + 4;
+    E.base = reinterpret_cast<int32_t*>(ws + l.base);
+    E.table = l.room > 0 ? reinterpret_cast<int32_t*>(ws + l.table) : nullptr;
+    E.room = l.room;
     E.q_stream = q_stream;
     E.q_pos = q_pos;
     E.n_q = n_q;
@@ -1297,8 +1322,16 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     E.window = win ? window : sh->capacity;
     E.n_sink = n_sink;
     E.pages = pg;
-    if (cudaMemsetAsync(E.range, 0, static_cast<size_t>(sh->n_streams) * 2 * sizeof(int32_t), s) != cudaSuccess)
+    // does the device have to choose, or do all blocks of all streams fit
+    const bool open = l.room > 0 && l.room < static_cast<int64_t>(sh->n_streams) * (sh->capacity / 128);
+    msa::Gate tile_gate;
+    if (open) {
+      tile_gate = {E.ctl + 1, msa::expand::kTiles};
+      cluster_gate = {E.ctl + 1, msa::expand::kCluster};
+    }
+    if (cudaMemsetAsync(ws, 0, (4 + static_cast<size_t>(sh->n_streams) * 2) * sizeof(int32_t), s) != cudaSuccess)
       return MSA_ERR_CUDA;
+    if (l.room == 0) E.ctl = nullptr;
     // about eight CTAs per SM, at most one per block of a stream and group
     const int64_t sg = static_cast<int64_t>(sh->n_streams) * G;
     const int64_t x = std::max<int64_t>(1, std::min<int64_t>(sh->capacity / 128, (8 * static_cast<int64_t>(sms) + sg - 1) / sg));
@@ -1307,15 +1340,22 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
                                                 static_cast<unsigned>(std::min<int64_t>(x, 65535))),
                dim3(256), 0, s, E) != cudaSuccess)
       return MSA_ERR_CUDA;
-    if (!win)
-      return sparse_attn(sh, q, reinterpret_cast<const msa_bf16*>(E.k_out), reinterpret_cast<const msa_bf16*>(E.v_out),
-                         a.sel, q_stream, q_pos, n_q, softmax_scale, out, ws + l.plans, l.k - l.plans, stream,
-                         MSA_MODE_PREFILL, pages);
-    return tile_attn(sh, q, E.k_out, E.v_out, pg, rows, q_stream, q_pos, n_q, window, n_sink, softmax_scale, out, sms, s);
+    const msa_pages own{E.table, static_cast<int32_t>(l.room)};
+    if (!win) {
+      st = sparse_attn(sh, q, reinterpret_cast<const msa_bf16*>(E.k_out), reinterpret_cast<const msa_bf16*>(E.v_out),
+                       a.sel, q_stream, q_pos, n_q, softmax_scale, out, ws + l.plans, l.k - l.plans, stream,
+                       MSA_MODE_PREFILL, l.room > 0 ? &own : pages, nullptr, nullptr, nullptr, nullptr, tile_gate);
+    } else {
+      msa::KvPages at = pg;
+      if (l.room > 0) at = {own.block_table, own.n_pages};
+      st = tile_attn(sh, q, E.k_out, E.v_out, at, l.rows, q_stream, q_pos, n_q, window, n_sink, softmax_scale, out, sms,
+                     tile_gate, s);
+    }
+    if (st != MSA_OK || !open) return st;
   }
   if (mode == MSA_MODE_PREFILL && !a.f8 && tiles_pay(sh, n_q))
     return tile_attn(sh, q, a.k_cache, a.v_cache, pg, rows, q_stream, q_pos, n_q, window, n_sink, softmax_scale, out,
-                     sms, s);
+                     sms, {}, s);
   CUtensorMap tm_k, tm_v;
   for (int i = 0; i < 2; ++i) {
     CUtensorMap* m = i == 0 ? &tm_k : &tm_v;
@@ -1340,6 +1380,7 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   P.n_sink = n_sink;
   P.scale_log2 = softmax_scale * 1.4426950408889634f;
   P.pages = pg;
+  P.gate = cluster_gate;
   const int64_t unit_rows = a.f8 ? msa::cattn::Unit<true>::kRows : msa::cattn::Unit<false>::kRows;
   // the most units a query can have
   const int64_t units = win ? std::min<int64_t>(sh->capacity / unit_rows, (P.window + unit_rows - 1) / unit_rows + 1 +

@@ -126,6 +126,7 @@ struct Params {
   int window, n_sink;         // window form
   float scale_log2;
   KvPages pages;
+  Gate gate;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, Unit<kF8>::kCtas)
   __syncthreads();
   pdl_trigger();
   pdl_wait();
+  if (!gate_open(P.gate)) return;                      // (the whole grid)
 
   const int qi = static_cast<int>(pair / P.G);
   const int g = static_cast<int>(pair - static_cast<long long>(qi) * P.G);

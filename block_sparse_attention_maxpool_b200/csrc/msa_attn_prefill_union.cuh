@@ -109,6 +109,7 @@ struct Params {
   float scale_log2;
   KvPages pages;             // kPaged: K/V are page pools addressed through the block table
   Plan* plans;               // [G * n_tiles]: written by plan_tiles_kernel, read by the attention kernel
+  Gate gate;                 // of both kernels
 };
 
 // Barrier slots (uint64 each, from Layout::kBarOff).
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(256) plan_tiles_kernel(const Params P) {
   pdl_trigger();
   pdl_wait();                                          // the selections come from the kernel before
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t < P.G * P.n_tiles) build_plan<kPaged>(P, t, P.plans[t], threadIdx.x & 31);
+  if (t < P.G * P.n_tiles && gate_open(P.gate)) build_plan<kPaged>(P, t, P.plans[t], threadIdx.x & 31);
 }
 
 template <bool kPaged>
@@ -427,7 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Bars B(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int n_tasks = P.G * P.n_tiles;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSBufs; ++i) {
@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *B.tmem_slot;
   pdl_trigger();
   pdl_wait();
+  const int n_tasks = gate_open(P.gate) ? P.G * P.n_tiles : 0;
 
   if (warp == 0) {
     // ------------------------ the Q tile and the K blocks (lane 0) ---------------------

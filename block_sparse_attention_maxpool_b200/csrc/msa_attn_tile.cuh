@@ -122,6 +122,7 @@ struct Params {
   int window, n_sink;
   float scale_log2;
   KvPages pages;
+  Gate gate;
 };
 
 struct Bars {
@@ -292,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Rec* recs = reinterpret_cast<const Rec*>(smem + L::kRecOff);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int n_tasks = P.G * P.n_tiles;
 
   if (threadIdx.x == 0) {
     mbar_init(B.q_full, 1);
@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *B.tmem_slot;
   pdl_trigger();
   pdl_wait();
+  const int n_tasks = gate_open(P.gate) ? P.G * P.n_tiles : 0;
 
   // The next record (every role keeps its own count of records read).
   auto next_rec = [&](int r, Rec& in) {

@@ -42,11 +42,19 @@ struct KvPages {
   int n_pages;
 };
 
+// A kernel that the device may leave out: it returns at once unless *choice
+// (written by a kernel before it) is `mine`.  Null: it runs.
+struct Gate {
+  const int32_t* choice = nullptr;
+  int32_t mine = 0;
+};
+__device__ __forceinline__ bool gate_open(const Gate& g) { return g.choice == nullptr || __ldcg(g.choice) == g.mine; }
+
 // First row of the block in the cache viewed as 2-D [rows][row]; -1 when a
 // paged cache maps the block to no valid page.
 __device__ __forceinline__ long long kv_block_row(const KvPages& pg, int s, int g, int b, int G, int capacity) {
   if (pg.table == nullptr) return (static_cast<long long>(s) * G + g) * capacity + static_cast<long long>(b) * 128;
-  const int page = __ldg(pg.table + static_cast<size_t>(s) * (capacity / 128) + b);
+  const int page = pg.table[static_cast<size_t>(s) * (capacity / 128) + b];   // (may be the work of the kernel before)
   if (page < 0 || page >= pg.n_pages) return -1;
   return (static_cast<long long>(page) * G + g) * 128;
 }

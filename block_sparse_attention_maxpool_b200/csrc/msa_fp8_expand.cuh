@@ -3,10 +3,16 @@
 // A prompt's tiles read a block many times (every 16 queries of a window read
 // it again, 8 queries of a selection share it at best), so the e4m3 values
 // are converted once per call, by a kernel of their own, into caches in the
-// caller's workspace with the 8-bit caches' layout (the same page table serves
-// both), which the bf16 prefill kernels read: bf16(scale * e4m3), exact when
-// the scale is a power of two, as the append writes it.  Only blocks that some
-// query of the call can see are touched.  Bound by bytes: 128 read and 256
+// caller's workspace, which the bf16 prefill kernels read: bf16(scale * e4m3),
+// exact when the scale is a power of two, as the append writes it.  Only blocks
+// that some query of the call can see are touched.  Small caches and pools
+// expand in place: the copy has their layout, and the same page table serves
+// both.  Of a large one the visible blocks go, stream by stream, into a pool of
+// `room` pages behind a table of the call's own; what does not fit there is
+// known on the device alone (the positions are), so the last CTA of the range
+// kernel adds the blocks up and chooses: the tiles, or the cluster kernel that
+// reads the 8-bit cache itself.  The kernels of the side that was not chosen
+// return at once.  Bound by bytes: 128 read and 256
 // written per row.  (Converted inside the attention kernel by four warps of
 // its own, block by block, the 2048-query selection on 16384 tokens took 1.04
 // ms instead of 0.66: the conversion of a block, about 4000 cycles next to the
@@ -28,12 +34,58 @@ struct Params {
   uint4* k_out;               // bf16, rows as in k_cache
   uint4* v_out;
   int32_t* range;             // [S][2], zeroed: highest position + 1, capacity - lowest slot seen
+  int32_t* ctl;               // [2]: CTAs of the range kernel that are done (zeroed), the choice (kTiles); null: neither
+  int32_t* base;              // [S]: first page of the stream's blocks
+  int32_t* table;             // [S][capacity / 128]: the call's own pages; null: laid out as the 8-bit cache
+  long long room;             // pages behind `table`
   const int32_t* q_stream;
   const int32_t* q_pos;
   int n_q, G, n_streams, capacity;
   int window, n_sink;         // selection form: window = capacity, n_sink = 0
   KvPages pages;
 };
+
+constexpr int32_t kCluster = 0, kTiles = 1;      // ctl[1]
+
+// The blocks that a stream's queries see: the sinks' that lie before the window's first, then the window's on.
+struct Visible {
+  int sinks, win, n;
+  __device__ Visible(const Params& P, int hi, int lo) {
+    const int first = P.capacity - lo;
+    win = first / 128;
+    sinks = min((P.n_sink + 127) / 128, win);
+    n = hi == 0 ? 0 : sinks + (hi - 1) / 128 - win + 1;
+  }
+  __device__ int block(int i) const { return i < sinks ? i : win + i - sinks; }
+};
+
+// The choice, and where each stream's blocks go (one CTA of 256 threads, the
+// ranges complete).
+__device__ void choose(const Params& P) {
+  __shared__ long long before[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long total = 0;
+  for (int s0 = 0; s0 < P.n_streams; s0 += 256) {
+    const int s = s0 + threadIdx.x;
+    const long long n = s < P.n_streams ? Visible(P, __ldcg(P.range + 2 * s), __ldcg(P.range + 2 * s + 1)).n : 0;
+    long long sum = n;                             // inclusive over the warp, then over the warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    if (lane == 31) before[warp] = sum;
+    __syncthreads();
+    long long at = total + sum - n;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) at += before[w];
+      total += before[w];
+    }
+    __syncthreads();
+    if (s < P.n_streams && P.table != nullptr) P.base[s] = static_cast<int32_t>(min(at, P.room));
+  }
+  if (threadIdx.x == 0) P.ctl[1] = P.table == nullptr || total <= P.room ? kTiles : kCluster;
+}
 
 // The slots that each stream's queries can see.
 __global__ void __launch_bounds__(256) expand_range_kernel(const Params P) {
@@ -53,6 +105,15 @@ __global__ void __launch_bounds__(256) expand_range_kernel(const Params P) {
     atomicMax(P.range + 2 * s, static_cast<int>(hi));
     atomicMax(P.range + 2 * s + 1, static_cast<int>(lo));
   }
+  if (P.ctl == nullptr) return;
+  __shared__ bool last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(P.ctl, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  choose(P);
 }
 
 // 16 e4m3 values times `f`, as bf16.
@@ -82,20 +143,22 @@ __global__ void __launch_bounds__(256) expand_kernel(const Params P) {
   pdl_trigger();
   pdl_wait();
   const int s = blockIdx.x, g = blockIdx.y;
+  if (P.ctl != nullptr && __ldcg(P.ctl + 1) != kTiles) return;
   const int hi = P.range[2 * s], first = P.capacity - P.range[2 * s + 1];
-  if (hi == 0) return;
-  const int win = first / 128;
-  const int sinks = min((P.n_sink + 127) / 128, win);
-  const int n = sinks + (hi - 1) / 128 - win + 1;
-  for (int i = blockIdx.z; i < n; i += gridDim.z) {
-    const int b = i < sinks ? i : win + i - sinks;
+  const Visible seen(P, hi, P.range[2 * s + 1]);
+  const int base = P.table != nullptr ? P.base[s] : 0;
+  for (int i = blockIdx.z; i < seen.n; i += gridDim.z) {
+    const int b = seen.block(i);
     const long long row = kv_block_row(P.pages, s, g, b, P.G, P.capacity);
+    if (P.table != nullptr && g == 0 && threadIdx.x == 0)
+      P.table[static_cast<size_t>(s) * (P.capacity / 128) + b] = row < 0 ? -1 : base + i;
     if (row < 0) continue;                       // the attention kernel reports it
+    const long long dst = P.table != nullptr ? (static_cast<long long>(base + i) * P.G + g) * 128 : row;
     const float ks = __ldcg(P.k_scale + row / 128), vs = __ldcg(P.v_scale + row / 128);
     const uint4* k = reinterpret_cast<const uint4*>(P.k_cache + row * 128);
     const uint4* v = reinterpret_cast<const uint4*>(P.v_cache + row * 128);
-    uint4* ko = P.k_out + row * 16;
-    uint4* vo = P.v_out + row * 16;
+    uint4* ko = P.k_out + dst * 16;
+    uint4* vo = P.v_out + dst * 16;
     uint4 x[4], y[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {

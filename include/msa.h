@@ -547,8 +547,13 @@ MSA_API int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages*
  * except for prefill calls over an 8-bit cache with many queries (1024
  * (query, group) pairs, 16 queries per stream on average): those may expand
  * the blocks that the call's queries can see to bf16 in the workspace, which
- * has room for the whole cache or pool (512 bytes per slot and group; one
- * buffer serves all layers of a model in turn).  Calls that may run at the
+ * has room for the whole cache or pool (512 bytes per slot and group) up to
+ * 1 GiB, and for 1 GiB of visible blocks of a larger one (plus 4 bytes per
+ * block of the streams' capacity).  Where a call sees more than that, or (for
+ * selected blocks) where few queries or a scale that is not positive make it
+ * pay, the kernel of the decode calls reads the 8-bit cache itself; a selection
+ * call that is sure not to expand needs no workspace.  One buffer serves all
+ * layers of a model in turn.  Calls that may run at the
  * same time on the GPU need separate workspaces. */
 MSA_API size_t msa_attn_workspace_bytes(const msa_shape* shape, const msa_pages* pages, int32_t n_q, int32_t mode,
                                         int32_t fp8);

@@ -121,3 +121,18 @@ def test_one_bufs_for_both_kinds_of_layers():
         out.append((msa.decode_step(shape, c, new, b, prefill=True)[0], msa.window_step(shape, c, new, 100, 4, b, prefill=True)))
     assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
     assert msa.msa_get_device_error() == 0
+
+
+def test_attention_workspace_of_large_caches_is_bounded(monkeypatch):
+    """The workspace of an 8-bit prompt grows with the cache up to 1 GiB of expanded rows, then stays (plus four bytes a
+    block of the table): a pool that fills the GPU needs no second one."""
+    G, n = 4, 2048
+    for shape, pages in ((msa.Shape(8, 131072), None), (msa.Shape(1, 131072 * 8), msa.CPages(0, 300000)),
+                         (msa.Shape(16, 131072), msa.CPages(0, 100000))):
+        blocks = shape.n_streams * shape.n_blocks
+        got = msa.library().msa_attn_workspace_bytes(shape.c(), pages, n, msa.MODE_PREFILL, 1)
+        room = min(blocks, (1 << 30) // (G * 128 * 512))
+        assert room * G * 128 * 512 <= got <= (1 << 30) + 4 * blocks + (8 << 20)
+    tiny = msa.Shape(2, 4096)
+    need = msa.msa_attn_workspace_bytes(tiny, n, msa.MODE_PREFILL, True)
+    assert 0 <= need - 2 * G * 4096 * 512 < 8 << 20

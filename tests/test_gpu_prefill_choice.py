@@ -75,3 +75,142 @@ def test_selection_without_tiles_needs_no_workspace(cap, scale):
     for fn in (msa.msa_sparse_attn_prefill_fp8, msa.msa_sparse_attn_decode_fp8):
         got = fn(shape, args[0], dev[0].view(F8), dev[1].view(F8), dev[2], dev[3], *args[2:5], softmax_scale=scale)
         assert torch.equal(got, out)
+
+
+# ---- caches whose expansion is larger than the workspace's 1 GiB: 2^21 slots of one group -----------------------------
+def codes(gen, *rows):
+    """Random e4m3 codes (no NaN) and scales of [..][rows][128] caches, on the GPU."""
+    x = torch.randint(0, 254, (*rows, 128), generator=gen, device="cuda", dtype=torch.uint8)
+    return torch.where(x >= 127, x + 1, x)
+
+
+def large_and_small(S, G, small, large, gen):
+    """Contiguous caches of the same rows in capacities ``small`` and ``large`` (NaN codes and scales behind them)."""
+    out = ([], [])
+    for _ in range(2):
+        x, sc = codes(gen, S, G, small), torch.exp2(torch.randint(-9, -5, (S, G, small // 128), generator=gen, device="cuda").float())
+        big = torch.full((S, G, large, 128), 0x7f, dtype=torch.uint8, device="cuda")
+        big[:, :, :small] = x
+        bsc = torch.full((S, G, large // 128), math.nan, device="cuda")
+        bsc[:, :, :small // 128] = sc
+        out[0].append((x.view(F8), sc))
+        out[1].append((big.view(F8), bsc))
+    return out
+
+
+def call(form, mode, shape, q, kv, stream, pos, sel, pages=None, window=1000, sink=130):
+    if form == "window":
+        fn = msa.msa_window_attn_prefill if mode == "prefill" else msa.msa_window_attn_decode
+        return fn(shape, q, kv[0][0], kv[1][0], stream, pos, window, sink, pages=pages, k_scale=kv[0][1], v_scale=kv[1][1])
+    fn = msa.msa_sparse_attn_prefill_fp8 if mode == "prefill" else msa.msa_sparse_attn_decode_fp8
+    return fn(shape, q, kv[0][0], kv[1][0], kv[0][1], kv[1][1], sel, stream, pos, pages=pages)
+
+
+def selections(n, G, pos, gen):
+    """16 visible blocks (or all) of each (query, group), the local one among them."""
+    nblk = int(pos.max()) // 128 + 1
+    b = torch.arange(nblk, device="cuda")
+    score = torch.rand((n, G, nblk), generator=gen, device="cuda")
+    local = (pos // 128)[:, None, None]
+    score = torch.where(b == local, 2.0, torch.where(b < local, score, -1.0))
+    best = score.topk(min(16, nblk), 2)
+    sel = torch.where(best.values >= 0, best.indices, -1).int()
+    return torch.nn.functional.pad(sel, (0, 16 - sel.shape[2]), value=-1).contiguous()
+
+
+@pytest.mark.parametrize("form", ["window", "selection"])
+def test_large_cache_expands_what_the_call_sees(form):
+    """2112 queries of 33 streams near the front of caches of 33 x 16384: the same bits as in caches of 33 x 2048, which
+    expand in place, with a workspace of little more than 1 GiB."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    S, G, small, large, per = 33, 4, 2048, 16384, 64
+    assert S * G * large * 512 > 1 << 30 > S * G * small * 512
+    kv = large_and_small(S, G, small, large, gen)
+    stream = torch.arange(S, device="cuda").repeat_interleave(per).int()
+    pos = (torch.arange(S, device="cuda")[:, None] * 53 % (small - per) + torch.arange(per, device="cuda")).flatten().int()
+    n = S * per
+    q = torch.randn((n, 16 * G, 128), generator=gen, device="cuda").bfloat16()
+    sel = selections(n, G, pos, gen)
+    assert (1 << 30) < msa.msa_attn_workspace_bytes(msa.Shape(S, large), n, msa.MODE_PREFILL, True) < 1.1 * (1 << 30)
+    want = call(form, "prefill", msa.Shape(S, small), q, kv[0], stream, pos, sel)
+    for _ in range(2):
+        assert torch.equal(call(form, "prefill", msa.Shape(S, large), q, kv[1], stream, pos, sel), want)
+    one = call(form, "decode", msa.Shape(S, small), q, kv[0], stream, pos, sel)
+    assert bool((want != one).any())          # (the kernels round differently: it was the tiles that ran)
+    PW.device_error()
+
+
+@pytest.mark.parametrize("form", ["window", "selection"])
+def test_large_cache_that_sees_too_much(form):
+    """More visible blocks than the workspace holds: the single-query kernel answers, bit for bit, also captured, and
+    next to a call that fits."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    S, G, cap, per = 33, 4, 16384, 64
+    shape = msa.Shape(S, cap)
+    kv = [(codes(gen, S, G, cap).view(F8), torch.exp2(torch.randint(-9, -5, (S, G, cap // 128), generator=gen, device="cuda").float()))
+          for _ in range(2)]
+    stream = torch.arange(S, device="cuda").repeat_interleave(per).int()
+    n = S * per
+    far = (cap - per + torch.arange(per, device="cuda")).repeat(S).int()
+    near = far - cap + 3000
+    pos = far.clone()
+    q = torch.randn((n, 16 * G, 128), generator=gen, device="cuda").bfloat16()
+    sel = torch.empty((n, G, 16), dtype=torch.int32, device="cuda")
+    ws = torch.empty(msa.msa_attn_workspace_bytes(shape, n, msa.MODE_PREFILL, True), dtype=torch.uint8, device="cuda")
+
+    def run(mode):
+        extra = dict(window=cap, sink=0) if form == "window" else {}
+        return call(form, mode, shape, q, kv, stream, pos, sel, **extra)
+    want = {}
+    for name, p in (("far", far), ("near", near)):
+        pos.copy_(p)
+        sel.copy_(selections(n, G, p, gen))
+        want[name] = (run("prefill"), run("decode"), sel.clone())
+    assert torch.equal(want["far"][0], want["far"][1])
+    assert bool((want["near"][0] != want["near"][1]).any())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run("prefill")
+    for name, p in (("near", near), ("far", far), ("near", near)):
+        pos.copy_(p)
+        sel.copy_(want[name][2])
+        graph.replay()
+        assert torch.equal(out, want[name][0])
+    PW.device_error()
+    del ws
+
+
+@pytest.mark.parametrize("form", ["window", "selection"])
+def test_large_pool_with_unmapped_and_shared_pages(form):
+    """Two streams over a pool of 4200 pages (more than the workspace's), one page of both, one missing, one out of
+    range: as over a pool of 40."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    G, per, nblk = 4, 700, 16
+    kv = [(codes(gen, 40, G, 128).view(F8), torch.exp2(torch.randint(-9, -5, (40, G), generator=gen, device="cuda").float()))
+          for _ in range(2)]
+    at = torch.randperm(4200, generator=gen, device="cuda")[:40]
+    big = []
+    for x, sc in kv:
+        y = torch.full((4200, G, 128, 128), 0x7f, dtype=torch.uint8, device="cuda")
+        y[at] = x.view(torch.uint8)
+        s = torch.full((4200, G), math.nan, device="cuda")
+        s[at] = sc
+        big.append((y.view(F8), s))
+    table = torch.randperm(40, generator=gen, device="cuda")[:2 * nblk].view(2, nblk).int()
+    table[1, 2] = table[0, 2]
+    far = at[table.long()].int()
+    for t, n_pages in ((table, 40), (far, 4200)):
+        t[0, 9] = -1
+        t[1, 11] = n_pages
+    stream = torch.tensor([0, 1], device="cuda").repeat_interleave(per).int()
+    pos = torch.cat((torch.arange(1300, 1300 + per, device="cuda"), torch.arange(1100, 1100 + per, device="cuda"))).int()
+    q = torch.randn((2 * per, 16 * G, 128), generator=gen, device="cuda").bfloat16()
+    sel = selections(2 * per, G, pos, gen)
+    shape = msa.Shape(2, nblk * 128)
+    want = call(form, "prefill", shape, q, kv, stream, pos, sel, msa.Pages(table, 40))
+    PW.device_error(0x10)
+    got = call(form, "prefill", shape, q, big, stream, pos, sel, msa.Pages(far, 4200))
+    PW.device_error(0x10)
+    assert torch.equal(got, want) and bool(want.isfinite().all())
+    # the workspace holds what the table can name, not the pool
+    assert msa.msa_attn_workspace_bytes(shape, 2 * per, msa.MODE_PREFILL, True, msa.Pages(far, 4200)) < 2 * nblk * G * 128 * 512 + (4 << 20)

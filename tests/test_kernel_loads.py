@@ -13,8 +13,8 @@ from tests import parity_window as PW
 from tests.test_gpu_fp8_cache import F8
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(msa.__file__)), "csrc")
-# what the caller's own kernels wrote before the call: tokens and queries, page tables, frequencies, head weights
-INPUTS = {"a", "c", "idx_src", "src", "tok_stream", "tok_pos", "P.q_stream", "P.q_pos", "pg.table", "r.inv_freq", "wp"}
+# what the caller's own kernels wrote before the call: tokens and queries, frequencies, head weights
+INPUTS = {"a", "c", "idx_src", "src", "tok_stream", "tok_pos", "P.q_stream", "P.q_pos", "r.inv_freq", "wp"}
 
 
 def test_only_inputs_are_read_non_coherently():
