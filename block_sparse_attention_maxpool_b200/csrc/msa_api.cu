@@ -1121,17 +1121,19 @@ bool expands(const msa_shape* sh, int32_t n_q, int mode, bool f8) {
          static_cast<int64_t>(n_q) >= int64_t{16} * std::min(sh->n_streams, n_q);
 }
 
-// Selected blocks: a tile of 8 queries reads the union of their selections,
-// about n (1 - (1 - 15 / n)^8) of n blocks where queries choose apart from one
-// another, one microsecond a block on 148 SMs; the cluster kernel reads each
-// query's 16 blocks, 0.085 us for a (query, group).  Measured (tiles /
-// cluster, us), 4 groups: 2048 queries on 4096 tokens 310 / 693, on 16384
-// 637 / 698, on 65536 841 / 700; 256 queries on 16384 161 / 107.
-bool selection_tiles_pay(const msa_shape* sh, int32_t n_q, int sms) {
-  const double nblk = sh->capacity / 128, pairs = static_cast<double>(n_q) * sh->n_kv_heads;
-  const double apart = nblk * (1.0 - std::pow(1.0 - std::min(1.0, 15.0 / nblk), 8.0));
-  const double waves = std::ceil(std::ceil(n_q / 8.0) * sh->n_kv_heads / sms);
-  return 70.0 + waves * apart < 10.0 + 0.085 * (148.0 / sms) * pairs * std::min(nblk, 16.0) / 16.0;
+// What a selection call does, by what the host knows: the queries see between
+// nothing and the capacity.
+enum class Choice { kTiles, kCluster, kDevice };
+Choice selection_choice(const msa_shape* sh, int32_t n_q, int sms) {
+  const int nblk = sh->capacity / 128;
+  const int64_t streams = std::min(sh->n_streams, n_q);
+  if (msa::expand::selection_tiles_pay(n_q, sh->n_kv_heads, nblk, streams * nblk, sms)) return Choice::kTiles;
+  // a short context of one stream; below 2048 pairs the choosing costs what it would save
+  const int few = std::min(nblk, 16);
+  if (static_cast<int64_t>(n_q) * sh->n_kv_heads < 2048 ||
+      !msa::expand::selection_tiles_pay(n_q, sh->n_kv_heads, few, few, sms))
+    return Choice::kCluster;
+  return Choice::kDevice;
 }
 
 // An expanded cache or pool larger than this goes into pages of the call's own,
@@ -1284,10 +1286,13 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   if ((st = pages_of(sh, pages, &pg, &rows)) != MSA_OK) return st;
   size_t need = ext_attn_workspace(sh, rows, n_q, mode, a.f8);
   int sms = 0;
+  bool by_context = false;
   // a selection that does not take the tiles needs no workspace (the selection tiles take a positive scale)
   if (!win && need > 0) {
     if ((st = current_device_sms(&sms)) != MSA_OK) return st;
-    if (!(softmax_scale > 0.f) || !selection_tiles_pay(sh, n_q, sms)) need = 0;
+    const Choice c = selection_choice(sh, n_q, sms);
+    if (!(softmax_scale > 0.f) || c == Choice::kCluster) need = 0;
+    by_context = c == Choice::kDevice;
   }
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return MSA_ERR_WORKSPACE;
@@ -1321,9 +1326,10 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     E.capacity = sh->capacity;
     E.window = win ? window : sh->capacity;
     E.n_sink = n_sink;
+    E.sms = by_context ? sms : 0;
     E.pages = pg;
     // does the device have to choose, or do all blocks of all streams fit
-    const bool open = l.room > 0 && l.room < static_cast<int64_t>(sh->n_streams) * (sh->capacity / 128);
+    const bool open = by_context || (l.room > 0 && l.room < static_cast<int64_t>(sh->n_streams) * (sh->capacity / 128));
     msa::Gate tile_gate;
     if (open) {
       tile_gate = {E.ctl + 1, msa::expand::kTiles};
@@ -1331,7 +1337,7 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     }
     if (cudaMemsetAsync(ws, 0, (4 + static_cast<size_t>(sh->n_streams) * 2) * sizeof(int32_t), s) != cudaSuccess)
       return MSA_ERR_CUDA;
-    if (l.room == 0) E.ctl = nullptr;
+    if (l.room == 0 && !open) E.ctl = nullptr;
     // about eight CTAs per SM, at most one per block of a stream and group
     const int64_t sg = static_cast<int64_t>(sh->n_streams) * G;
     const int64_t x = std::max<int64_t>(1, std::min<int64_t>(sh->capacity / 128, (8 * static_cast<int64_t>(sms) + sg - 1) / sg));

@@ -8,12 +8,14 @@
 // that some query of the call can see are touched.  Small caches and pools
 // expand in place: the copy has their layout, and the same page table serves
 // both.  Of a large one the visible blocks go, stream by stream, into a pool of
-// `room` pages behind a table of the call's own; what does not fit there is
-// known on the device alone (the positions are), so the last CTA of the range
-// kernel adds the blocks up and chooses: the tiles, or the cluster kernel that
-// reads the 8-bit cache itself.  The kernels of the side that was not chosen
-// return at once.  Bound by bytes: 128 read and 256
-// written per row.  (Converted inside the attention kernel by four warps of
+// `room` pages behind a table of the call's own.  What the queries see only the
+// device knows (the positions are there, and a captured call is replayed with
+// others), so where it matters the last CTA of the range kernel adds the blocks
+// up and chooses: the tiles, or the cluster kernel that reads the 8-bit cache
+// itself, where the blocks do not fit or a selection over many of them takes
+// less time there.  The kernels of the side that was not chosen return at once
+// (9 to 14 us in all, 2112 queries).  Bound by bytes: 128 read and 256 written
+// per row.  (Converted inside the attention kernel by four warps of
 // its own, block by block, the 2048-query selection on 16384 tokens took 1.04
 // ms instead of 0.66: the conversion of a block, about 4000 cycles next to the
 // softmax warps, paced the loop.)
@@ -25,6 +27,32 @@
 
 namespace msa {
 namespace expand {
+
+// Selected blocks: whether the union tiles take less time than the cluster
+// kernel, for n_q queries that see `total` blocks, `top` at most in one stream.
+// A tile of 8 queries reads the union of their selections, about
+// top (1 - (1 - 15 / top)^8) blocks where queries choose apart from one another,
+// one microsecond a block on 148 SMs, behind the expansion of all that is seen
+// (96 KB of traffic per block and group); the cluster kernel reads each query's
+// 16 blocks, 0.085 us for a (query, group).  Measured, 4 groups, one stream
+// (tiles / cluster, us, back to back), by the tokens that the queries see:
+//
+//   queries     1024         4096         16384         65536
+//       256    36 /  59     68 /  89    123 /   89    179 /   91
+//       512    48 / 103    107 / 171    193 /  171    277 /  174
+//      1024    68 / 174    181 / 336    334 /  336    469 /  341
+//      2048                267 / 666    579 /  668    774 /  672
+//      4096                391 / 1119  1101 / 1329   1502 / 1331
+//
+// and 1920 queries of 30 streams on 2048 tokens 244 / 635, on 4096 422 / 635, on
+// 16384 927 / 636.
+__host__ __device__ inline bool selection_tiles_pay(int n_q, int G, int top, long long total, int sms) {
+  const float blocks = static_cast<float>(top), pairs = static_cast<float>(n_q) * G;
+  const float miss = 1.f - fminf(1.f, 15.f / blocks), miss2 = miss * miss, miss4 = miss2 * miss2;
+  const float rounds = ceilf(ceilf(n_q / 8.f) * G / sms);
+  const float tiles = 40.f + rounds * blocks * (1.f - miss4 * miss4) + 0.023f * static_cast<float>(total) * G;
+  return tiles < 10.f + 0.085f * (148.f / sms) * pairs * fminf(blocks, 16.f) / 16.f;
+}
 
 struct Params {
   const uint8_t* k_cache;
@@ -42,6 +70,7 @@ struct Params {
   const int32_t* q_pos;
   int n_q, G, n_streams, capacity;
   int window, n_sink;         // selection form: window = capacity, n_sink = 0
+  int sms;                    // selection form that the device chooses by what is seen; else 0
   KvPages pages;
 };
 
@@ -63,11 +92,15 @@ struct Visible {
 // ranges complete).
 __device__ void choose(const Params& P) {
   __shared__ long long before[8];
+  __shared__ int top;
+  if (threadIdx.x == 0) top = 0;
+  __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long total = 0;
   for (int s0 = 0; s0 < P.n_streams; s0 += 256) {
     const int s = s0 + threadIdx.x;
     const long long n = s < P.n_streams ? Visible(P, __ldcg(P.range + 2 * s), __ldcg(P.range + 2 * s + 1)).n : 0;
+    if (n > 0) atomicMax(&top, static_cast<int>(n));
     long long sum = n;                             // inclusive over the warp, then over the warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -84,7 +117,10 @@ __device__ void choose(const Params& P) {
     __syncthreads();
     if (s < P.n_streams && P.table != nullptr) P.base[s] = static_cast<int32_t>(min(at, P.room));
   }
-  if (threadIdx.x == 0) P.ctl[1] = P.table == nullptr || total <= P.room ? kTiles : kCluster;
+  if (threadIdx.x != 0) return;
+  bool tiles = P.table == nullptr || total <= P.room;
+  if (tiles && P.sms > 0 && total > 0) tiles = selection_tiles_pay(P.n_q, P.G, top, total, P.sms);
+  P.ctl[1] = tiles ? kTiles : kCluster;
 }
 
 // The slots that each stream's queries can see.

@@ -214,3 +214,40 @@ def test_large_pool_with_unmapped_and_shared_pages(form):
     assert torch.equal(got, want) and bool(want.isfinite().all())
     # the workspace holds what the table can name, not the pool
     assert msa.msa_attn_workspace_bytes(shape, 2 * per, msa.MODE_PREFILL, True, msa.Pages(far, 4200)) < 2 * nblk * G * 128 * 512 + (4 << 20)
+
+
+@pytest.mark.parametrize("S,per,cap", [(1, 2048, 131072), (16, 128, 16384)])
+def test_selection_chooses_by_what_the_queries_see(S, per, cap):
+    """2048 queries of one stream or of 16, near the front (the tiles answer) and far behind (the cluster kernel
+    does): the bits of each kernel, in one captured call whose positions change."""
+    gen = torch.Generator(device="cuda").manual_seed(11 + S)
+    G, small = 4, 4096
+    shape, n = msa.Shape(S, cap), S * per
+    kv = [(codes(gen, S, G, cap).view(F8), torch.exp2(torch.randint(-9, -5, (S, G, cap // 128), generator=gen, device="cuda").float()))
+          for _ in range(2)]
+    front = [(x.view(torch.uint8)[:, :, :small].contiguous().view(F8), s[:, :, :small // 128].contiguous()) for x, s in kv]
+    stream = torch.arange(S, device="cuda").repeat_interleave(per).int()
+    near = (1900 + torch.arange(per, device="cuda")).repeat(S).int()
+    far = near + (cap - 1900 - per)
+    q = torch.randn((n, 16 * G, 128), generator=gen, device="cuda").bfloat16()
+    pos, sel = near.clone(), selections(n, G, near, gen)
+    want = {}
+    for name, p in (("near", near), ("far", far)):
+        pos.copy_(p)
+        sel.copy_(selections(n, G, p, gen))
+        one = call("selection", "decode", shape, q, kv, stream, pos, sel)
+        got = call("selection", "prefill", shape, q, kv, stream, pos, sel)
+        want[name] = (got, sel.clone())
+        assert torch.equal(got, one) == (name == "far")
+    sel.copy_(want["near"][1])
+    # the same rows in a cache of the context's size, where the host is sure of the tiles
+    assert torch.equal(call("selection", "prefill", msa.Shape(S, small), q, front, stream, near, sel), want["near"][0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call("selection", "prefill", shape, q, kv, stream, pos, sel)
+    for name, p in (("near", near), ("far", far), ("near", near)):
+        pos.copy_(p)
+        sel.copy_(want[name][1])
+        graph.replay()
+        assert torch.equal(out, want[name][0])
+    PW.device_error()
