@@ -1103,14 +1103,27 @@ int make_map_8bit(CUtensorMap* m, const void* base, int64_t rows) {
 
 // Which kernel a prefill call takes.  The tensor-core tiles need queries that
 // share blocks, and enough of them: by the counts alone, since positions are
-// on the device.  A call with fewer than four queries per stream on average
-// (and than one wave of work) takes the cluster kernel, a (query, group) per
-// cluster.  Measured on 148 SMs, cluster kernel against tiles (us): bf16, 4
-// groups, window 1024: 64 queries 33 / 43, 128 52 / 46, 512 132 / 47; window
-// 128: 128 31 / 31, 512 62 / 32; 32 streams of 16 queries 133 / 49, of 2 36 / 156.
+// on the device.  A tile of 16 queries walks the blocks of every stream in it,
+// so queries that are alone in their streams make it slow; but the streams of
+// the shape are slots of the cache, and a prompt may be the only one in its
+// call.  So the share of a slot counts only below 2048 (query, group) pairs
+// (where one wave of tiles begins to fill the SMs, and a wrong choice costs
+// least).  Measured, bf16, 4 groups (cluster kernel / tiles, us):
+//
+//   streams x queries   window 128    window 1024    window 4096   window 32768
+//              1 x 64    12 /  19      23 /  33       55 /  80      367 /  516
+//              1 x 128   19 /  18      39 /  33      107 /  82      709 /  519
+//              1 x 512   53 /  20     121 /  35      348 /  86     2451 /  524
+//              1 x 1024  98 /  31     231 /  61      686 / 160     4842 / 1034
+//             32 x 16    51 /  23     119 /  37
+//             64 x 4     31 /  37      70 /  78      201 / 221
+//            128 x 4     53 /  41     123 /  84
+//            256 x 1     37 /  74     107 / 242      328 / 824
+//            256 x 2     57 /  66     135 / 152
+//            512 x 1     60 /  76     188 / 250
 bool tiles_pay(const msa_shape* sh, int32_t n_q) {
-  return static_cast<int64_t>(n_q) * sh->n_kv_heads >= 512 &&
-         static_cast<int64_t>(n_q) >= int64_t{4} * std::min(sh->n_streams, n_q);
+  const int64_t pairs = static_cast<int64_t>(n_q) * sh->n_kv_heads;
+  return pairs >= 2048 || (pairs >= 512 && n_q >= int64_t{4} * std::min(sh->n_streams, n_q));
 }
 
 // Prefill calls over an 8-bit cache expand it to bf16 before they take the

@@ -251,3 +251,35 @@ def test_selection_chooses_by_what_the_queries_see(S, per, cap):
         graph.replay()
         assert torch.equal(out, want[name][0])
     PW.device_error()
+
+
+def one_prompt_in_many_slots(slots, cap, per, gen, f8):
+    """The queries of one prompt in a pool that ``slots`` streams share, and as the only stream of a small one: (shape,
+    pages, stream) of both, and the caches, positions and queries."""
+    G, nblk, n_pages = 4, cap // 128, cap // 128 + 3
+    kv = []
+    for _ in range(2):
+        if f8:
+            kv.append((codes(gen, n_pages, G, 128).view(F8), torch.exp2(torch.randint(-9, -5, (n_pages, G), generator=gen,
+                                                                                      device="cuda").float())))
+        else:
+            kv.append((torch.randn((n_pages, G, 128, 128), generator=gen, device="cuda").bfloat16(), None))
+    table = torch.full((slots, nblk), -1, dtype=torch.int32, device="cuda")
+    mine = slots * 2 // 3
+    table[mine] = torch.randperm(n_pages, generator=gen, device="cuda")[:nblk].int()
+    alone = msa.Pages(table[mine:mine + 1].contiguous(), n_pages)
+    pos = (cap - per + torch.arange(per, device="cuda")).int()
+    q = torch.randn((per, 16 * G, 128), generator=gen, device="cuda").bfloat16()
+    zero = torch.zeros(per, dtype=torch.int32, device="cuda")
+    return ((msa.Shape(slots, cap), msa.Pages(table, n_pages), zero + mine), (msa.Shape(1, cap), alone, zero)), kv, pos, q
+
+
+def test_one_prompt_in_a_cache_of_many_slots():
+    """1024 queries of one stream, window over bf16: the tiles answer, however many slots the cache has."""
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    (many, alone), kv, pos, q = one_prompt_in_many_slots(512, 2048, 1024, gen, False)
+    run = lambda mode, at: call("window", mode, at[0], q, kv, at[2], pos, None, at[1])
+    want = run("prefill", alone)
+    assert torch.equal(run("prefill", many), want)
+    assert bool((run("decode", alone) != want).any())
+    PW.device_error()
