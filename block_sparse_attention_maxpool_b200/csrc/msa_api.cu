@@ -1127,11 +1127,28 @@ bool tiles_pay(const msa_shape* sh, int32_t n_q) {
 }
 
 // Prefill calls over an 8-bit cache expand it to bf16 before they take the
-// tiles, which wants more queries: window 1024: 64 queries 37 / 67, 256 82 /
-// 67; window 4096: 64 71 / 121, 256 195 / 123, 1024 676 / 203.
+// tiles, which wants more queries.  Measured, window, 4 groups (cluster kernel /
+// expansion and tiles, us):
+//
+//   streams x queries   window 128    window 1024    window 4096   window 32768
+//              1 x 128   20 /  24      39 /  39      103 /  89      690 /  548
+//              1 x 256   33 /  26      66 /  40      180 /  90     1229 /  549
+//              1 x 1024 107 /  37     229 /  67      658 / 167     4606 / 1053
+//             64 x 4     35 /  59      66 / 134      178 / 404
+//             64 x 16   104 /  53     227 / 120      654 / 355
+//            256 x 4    105 / 132     227 / 365
+//            512 x 1     59 / 166     131 / 627
+//
+// Sixteen queries per slot of the cache are enough for sure.  From 1024 queries
+// on a prompt that has many slots to itself is worth the device's choice, by the
+// streams that the queries come from.
+constexpr int kExpandShare = 16;
+bool expands_for_sure(const msa_shape* sh, int32_t n_q) {
+  return static_cast<int64_t>(n_q) >= int64_t{kExpandShare} * std::min(sh->n_streams, n_q);
+}
 bool expands(const msa_shape* sh, int32_t n_q, int mode, bool f8) {
   return f8 && mode == MSA_MODE_PREFILL && static_cast<int64_t>(n_q) * sh->n_kv_heads >= 1024 &&
-         static_cast<int64_t>(n_q) >= int64_t{16} * std::min(sh->n_streams, n_q);
+         (n_q >= 1024 || expands_for_sure(sh, n_q));
 }
 
 // What a selection call does, by what the host knows: the queries see between
@@ -1307,9 +1324,14 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     if (!(softmax_scale > 0.f) || c == Choice::kCluster) need = 0;
     by_context = c == Choice::kDevice;
   }
+  const bool by_streams = !expands_for_sure(sh, n_q);
   if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need) return MSA_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MSA_ERR_ALIGN;
+    if (workspace == nullptr || workspace_bytes < need) {
+      if (!by_streams) return MSA_ERR_WORKSPACE;
+      need = 0;                                  // the cluster kernel does it too
+    } else if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) {
+      return MSA_ERR_ALIGN;
+    }
   }
   if (sms == 0 && (st = current_device_sms(&sms)) != MSA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1340,9 +1362,10 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     E.window = win ? window : sh->capacity;
     E.n_sink = n_sink;
     E.sms = by_context ? sms : 0;
+    E.share = by_streams ? kExpandShare : 0;
     E.pages = pg;
     // does the device have to choose, or do all blocks of all streams fit
-    const bool open = by_context || (l.room > 0 && l.room < static_cast<int64_t>(sh->n_streams) * (sh->capacity / 128));
+    const bool open = by_context || by_streams || (l.room > 0 && l.room < static_cast<int64_t>(sh->n_streams) * (sh->capacity / 128));
     msa::Gate tile_gate;
     if (open) {
       tile_gate = {E.ctl + 1, msa::expand::kTiles};

@@ -12,8 +12,8 @@
 // device knows (the positions are there, and a captured call is replayed with
 // others), so where it matters the last CTA of the range kernel adds the blocks
 // up and chooses: the tiles, or the cluster kernel that reads the 8-bit cache
-// itself, where the blocks do not fit or a selection over many of them takes
-// less time there.  The kernels of the side that was not chosen return at once
+// itself, where the blocks do not fit, the queries come from too many streams or
+// a selection over many blocks takes less time there.  The kernels of the side that was not chosen return at once
 // (9 to 14 us in all, 2112 queries).  Bound by bytes: 128 read and 256 written
 // per row.  (Converted inside the attention kernel by four warps of
 // its own, block by block, the 2048-query selection on 16384 tokens took 1.04
@@ -70,6 +70,7 @@ struct Params {
   const int32_t* q_pos;
   int n_q, G, n_streams, capacity;
   int window, n_sink;         // selection form: window = capacity, n_sink = 0
+  int share;                  // queries per stream that the tiles want; 0: the host has seen to it
   int sms;                    // selection form that the device chooses by what is seen; else 0
   KvPages pages;
 };
@@ -92,15 +93,18 @@ struct Visible {
 // ranges complete).
 __device__ void choose(const Params& P) {
   __shared__ long long before[8];
-  __shared__ int top;
-  if (threadIdx.x == 0) top = 0;
+  __shared__ int top, streams;
+  if (threadIdx.x == 0) top = streams = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long total = 0;
   for (int s0 = 0; s0 < P.n_streams; s0 += 256) {
     const int s = s0 + threadIdx.x;
     const long long n = s < P.n_streams ? Visible(P, __ldcg(P.range + 2 * s), __ldcg(P.range + 2 * s + 1)).n : 0;
-    if (n > 0) atomicMax(&top, static_cast<int>(n));
+    if (n > 0) {
+      atomicMax(&top, static_cast<int>(n));
+      atomicAdd(&streams, 1);
+    }
     long long sum = n;                             // inclusive over the warp, then over the warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -118,7 +122,7 @@ __device__ void choose(const Params& P) {
     if (s < P.n_streams && P.table != nullptr) P.base[s] = static_cast<int32_t>(min(at, P.room));
   }
   if (threadIdx.x != 0) return;
-  bool tiles = P.table == nullptr || total <= P.room;
+  bool tiles = (P.table == nullptr || total <= P.room) && P.n_q >= static_cast<long long>(P.share) * streams;
   if (tiles && P.sms > 0 && total > 0) tiles = selection_tiles_pay(P.n_q, P.G, top, total, P.sms);
   P.ctl[1] = tiles ? kTiles : kCluster;
 }

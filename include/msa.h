@@ -545,14 +545,16 @@ MSA_API int msa_window_attn_prefill_fp8(const msa_shape* shape, const msa_pages*
  * (fp8 nonzero) an 8-bit cache, contiguous (pages NULL) or paged (only
  * pages->n_pages is read); (size_t)-1 for unsupported arguments.  It is 0
  * except for prefill calls over an 8-bit cache with many queries (1024
- * (query, group) pairs, 16 queries per stream on average): those may expand
- * the blocks that the call's queries can see to bf16 in the workspace, which
+ * (query, group) pairs, 16 queries per stream of the shape on average or 1024
+ * in all): those may expand the blocks that the call's queries can see to bf16 in the workspace, which
  * has room for the whole cache or pool (512 bytes per slot and group) up to
  * 1 GiB, and for 1 GiB of visible blocks of a larger one (plus 4 bytes per
- * block of the streams' capacity).  Where a call sees more than that, or (for
- * selected blocks) where few queries or a scale that is not positive make it
+ * block of the streams' capacity).  Where a call sees more than that, has fewer
+ * than 16 queries per stream that it names, or (for selected blocks) where few queries or a scale that is not positive make it
  * pay, the kernel of the decode calls reads the 8-bit cache itself; a selection
- * call that is sure not to expand needs no workspace.  One buffer serves all
+ * call that is sure not to expand needs no workspace, and a call with fewer than
+ * 16 queries per stream of the shape does without one (the kernel of the decode
+ * calls answers).  One buffer serves all
  * layers of a model in turn.  Calls that may run at the
  * same time on the GPU need separate workspaces. */
 MSA_API size_t msa_attn_workspace_bytes(const msa_shape* shape, const msa_pages* pages, int32_t n_q, int32_t mode,

@@ -283,3 +283,33 @@ def test_one_prompt_in_a_cache_of_many_slots():
     assert torch.equal(run("prefill", many), want)
     assert bool((run("decode", alone) != want).any())
     PW.device_error()
+
+
+@pytest.mark.parametrize("form", ["window", "selection"])
+def test_8bit_prompts_in_a_cache_of_many_slots(form):
+    """1024 queries over 8-bit pages of 256 slots, 4 per slot: those of one stream take the tiles, those of all streams
+    the cluster kernel, in one captured call; without a workspace the cluster kernel answers."""
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    slots, cap, n = 256, 2048, 1024
+    (many, alone), kv, pos, q = one_prompt_in_many_slots(slots, cap, n, gen, True)
+    shape, pages, stream = many
+    pages.block_table[:] = pages.block_table[slots * 2 // 3]               # the other slots share its pages
+    sel = selections(n, 4, pos, gen)
+    run = lambda mode, at: call(form, mode, at[0], q, kv, at[2], pos, sel, at[1])
+    want, one = run("prefill", alone), run("decode", alone)
+    assert bool((want != one).any())
+    scattered = (torch.arange(n, device="cuda") % slots).int()
+    mine = stream.clone()
+    graph = torch.cuda.CUDAGraph()
+    assert torch.equal(run("prefill", many), want)
+    with torch.cuda.graph(graph):
+        out = run("prefill", many)
+    for s, result in ((mine, want), (scattered, one), (mine, want)):
+        stream.copy_(s)
+        graph.replay()
+        assert torch.equal(out, result)
+    if form == "selection":
+        out.fill_(math.nan)
+        assert raw_sparse(shape, q, [kv[0][0], kv[1][0], kv[0][1], kv[1][1]], sel, stream, pos, 128 ** -0.5, out, pages=pages) == 0
+        assert torch.equal(out, one)
+    PW.device_error()
