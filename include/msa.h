@@ -489,7 +489,11 @@ MSA_API size_t msa_kv_append_fp8_workspace_bytes(const msa_shape* shape, int32_t
  * of msa_sparse_attn_decode over an 8-bit cache, for a few queries and for
  * batches of many; same selection, layouts, rounding of the output and
  * errors.  The products see the e4m3 values exactly; softmax, sums and the
- * scales are float32.  The prefill call takes scale * e4m3 as bf16 when it
+ * scales are float32.  A row's weight times its V scale is rounded to 11 bits
+ * (fp16) where the 8-bit cache is read itself, as the decode calls do: from the
+ * largest such product of the query and head down to 2^-24 of it; smaller ones
+ * are off by at most 2^-35 of it.  Where it is expanded the weights are rounded
+ * to 8 bits (bf16).  The prefill call takes scale * e4m3 as bf16 when it
  * expands the cache (see msa_attn_workspace_bytes): exact for scales that are
  * powers of two, as msa_kv_append_fp8 writes them, else one more rounding.
  * pages may be NULL.  workspace: at least msa_attn_workspace_bytes(shape,
