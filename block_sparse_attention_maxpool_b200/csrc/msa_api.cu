@@ -1361,6 +1361,7 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
     E.capacity = sh->capacity;
     E.window = win ? window : sh->capacity;
     E.n_sink = n_sink;
+    E.clean = !win;
     E.sms = by_context ? sms : 0;
     E.share = by_streams ? kExpandShare : 0;
     E.pages = pg;

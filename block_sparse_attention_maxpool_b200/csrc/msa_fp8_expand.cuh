@@ -70,6 +70,7 @@ struct Params {
   const int32_t* q_pos;
   int n_q, G, n_streams, capacity;
   int window, n_sink;         // selection form: window = capacity, n_sink = 0
+  bool clean;                 // selection form: NaN in V rows that the stream's queries do not see becomes zero
   int share;                  // queries per stream that the tiles want; 0: the host has seen to it
   int sms;                    // selection form that the device chooses by what is seen; else 0
   KvPages pages;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(256) expand_kernel(const Params P) {
   pdl_wait();
   const int s = blockIdx.x, g = blockIdx.y;
   if (P.ctl != nullptr && __ldcg(P.ctl + 1) != kTiles) return;
-  const int hi = P.range[2 * s], first = P.capacity - P.range[2 * s + 1];
+  const int hi = P.range[2 * s];
   const Visible seen(P, hi, P.range[2 * s + 1]);
   const int base = P.table != nullptr ? P.base[s] : 0;
   for (int i = blockIdx.z; i < seen.n; i += gridDim.z) {
@@ -207,11 +208,11 @@ __global__ void __launch_bounds__(256) expand_kernel(const Params P) {
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      // V rows that no query of the stream sees may hold NaN, which times a
-      // weight of zero would still be NaN (other streams that share the page
-      // write the same values, but for such a NaN)
-      const int j = b * 128 + (threadIdx.x + 256 * c) / 8;
-      if (j >= hi || (j < first && j >= P.n_sink))
+      // V rows past every query of the stream may hold NaN, which times a weight
+      // of zero would still be NaN in the union tiles (the window tiles clear
+      // what they do not see; streams that share the page write the same
+      // values, but for such a NaN)
+      if (P.clean && b * 128 + static_cast<int>(threadIdx.x + 256 * c) / 8 >= hi)
         y[c] = make_uint4(without_nan(y[c].x), without_nan(y[c].y), without_nan(y[c].z), without_nan(y[c].w));
       const int at = (threadIdx.x + 256 * c) * 2;
       uint4 a, d;

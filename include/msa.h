@@ -495,7 +495,9 @@ MSA_API size_t msa_kv_append_fp8_workspace_bytes(const msa_shape* shape, int32_t
  * are off by at most 2^-35 of it.  Where it is expanded the weights are rounded
  * to 8 bits (bf16).  The prefill call takes scale * e4m3 as bf16 when it
  * expands the cache (see msa_attn_workspace_bytes): exact for scales that are
- * powers of two, as msa_kv_append_fp8 writes them, else one more rounding.
+ * powers of two, as msa_kv_append_fp8 writes them, else one more rounding; a
+ * NaN in a V row past the last query of one of the streams that share a page may
+ * then be left out for the others too.
  * pages may be NULL.  workspace: at least msa_attn_workspace_bytes(shape,
  * pages, n_q, mode, 1) bytes, 256-byte aligned (NULL when that is 0). */
 MSA_API int msa_sparse_attn_decode_fp8(const msa_shape* shape, const msa_pages* pages, const msa_bf16* q,

@@ -313,3 +313,28 @@ def test_8bit_prompts_in_a_cache_of_many_slots(form):
         assert raw_sparse(shape, q, [kv[0][0], kv[1][0], kv[0][1], kv[1][1]], sel, stream, pos, 128 ** -0.5, out, pages=pages) == 0
         assert torch.equal(out, one)
     PW.device_error()
+
+
+def test_a_nan_that_one_of_two_streams_sees():
+    """Two streams share a page, only one of them sees the row whose V is NaN: its queries say so, in every call, and the
+    other's are as without it (window over 8-bit pages, expanded in place)."""
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    G, n = 4, 512
+    shape = msa.Shape(2, 512)
+    kv = [(codes(gen, 6, G, 128).view(F8), torch.full((6, G), 2.0 ** -8, device="cuda")) for _ in range(2)]
+    table = torch.tensor([[3, 1, -1, -1], [3, 1, 5, 0]], dtype=torch.int32, device="cuda")
+    stream = (torch.arange(n, device="cuda") // 256).int()
+    i = torch.arange(256, device="cuda")
+    pos = torch.cat((i % 60 + 130, 384 + i % 120)).int()                  # stream 0 ends inside the second page
+    q = torch.randn((n, 16 * G, 128), generator=gen, device="cuda").bfloat16()
+    run = lambda: call("window", "prefill", shape, q, kv, stream, pos, None, msa.Pages(table, 6), window=512, sink=0)
+    clean = run()
+    kv[1][0].view(torch.uint8)[1, 2, 100, 7] = 0x7f                         # slot 228 of both, group 2
+    for _ in range(20):
+        out = run()
+        bad = out.isnan()
+        assert bool(bad[256:, 32:48, 7].all())
+        bad[256:, 32:48, 7] = False
+        assert not bool(bad.any())
+        assert torch.equal(out[:256], clean[:256])
+    PW.device_error()
