@@ -254,6 +254,8 @@ __global__ void __launch_bounds__(kThreads, Unit<kF8>::kCtas)
 
   if (warp == kWarps) {
     // ------------- producer: 32 units resolved at a time, one per lane -------------
+    // a block that the selection names again counts once
+    if (!kWin && (__match_any_sync(0xffffffffu, picked) & ((1u << (lane & (kTopK - 1))) - 1u)) != 0u) picked = -1;
     int k = 0;
     bool ok = true;
     for (int base = u0; base < u1 && ok; base += 32) {

@@ -488,7 +488,7 @@ MSA_API size_t msa_kv_append_fp8_workspace_bytes(const msa_shape* shape, int32_t
 /* msa_sparse_attn_decode_fp8, msa_sparse_attn_prefill_fp8 - the computation
  * of msa_sparse_attn_decode over an 8-bit cache, for a few queries and for
  * batches of many; same selection, layouts, rounding of the output and
- * errors.  The products see the e4m3 values exactly; softmax, sums and the
+ * errors (a block that sel names twice counts once).  The products see the e4m3 values exactly; softmax, sums and the
  * scales are float32.  A row's weight times its V scale is rounded to 11 bits
  * (fp16) where the 8-bit cache is read itself, as the decode calls do: from the
  * largest such product of the query and head down to 2^-24 of it; smaller ones

@@ -338,3 +338,35 @@ def test_a_nan_that_one_of_two_streams_sees():
         assert not bool(bad.any())
         assert torch.equal(out[:256], clean[:256])
     PW.device_error()
+
+
+def test_a_block_named_twice_counts_once():
+    """Selections that name a block several times, in single-query and prompt calls, of the tiles and of the cluster
+    kernel: the rows of the blocks in sel, each once."""
+    gen = torch.Generator().manual_seed(41)
+    G, cap, n = 4, 2048, 256
+    shape = msa.Shape(1, cap)
+    kv = caches(1, G, cap, gen)
+    pos = (1500 + torch.arange(n)).int()
+    stream = torch.zeros(n, dtype=torch.int32)
+    sel = torch.randint(-1, 11, (n, G, 16), generator=gen).int()
+    sel[::3, :, 5] = sel[::3, :, 9]
+    sel[1] = 7
+    q = torch.randn((n, 16 * G, 128), generator=gen).bfloat16()
+    once = sel.clone()
+    for i in range(n):
+        for g in range(G):
+            seen = set()
+            for j in range(16):
+                b = int(sel[i, g, j])
+                once[i, g, j] = -1 if b in seen else b
+                seen.add(b)
+    dev = [x.cuda() for x in (kv[0][0], kv[1][0], kv[0][1], kv[1][1])]
+    some = torch.arange(0, n, 9)
+    want = C.selected_attention(q[some], kv[0][2], kv[1][2], once[some], stream[some], pos[some], 128 ** -0.5)
+    for fn in (msa.msa_sparse_attn_decode_fp8, msa.msa_sparse_attn_prefill_fp8):
+        a, b = (fn(shape, q.cuda(), dev[0].view(F8), dev[1].view(F8), dev[2], dev[3], x.cuda(), stream.cuda(), pos.cuda())
+                for x in (sel, once))
+        PW.check_attention(a[some.cuda()], *want, PW.P_BF16, 0.0, PW.P_FP16)
+        PW.check_attention(b[some.cuda()], *want, PW.P_BF16, 0.0, PW.P_FP16)
+    PW.device_error()
