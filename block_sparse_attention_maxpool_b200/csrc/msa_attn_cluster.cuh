@@ -37,8 +37,8 @@
 //
 // Measured: bf16, 32 queries x 4 groups, window 4096 in shuffled pages: 49.7
 // us, 5.4 TB/s (0.83 of the measured copy rate).  e4m3: window 32768, 8
-// queries x 4 groups: 56 us, 4.8 TB/s; 16 selected blocks, 32 queries x 4
-// groups: 21.9 us, 3.1 TB/s.  Loads, start and merge alone take 82 to 88 % of
+// queries x 4 groups: 58 us, 4.6 TB/s; 16 selected blocks, 32 queries x 4
+// groups: 21.8 us, 3.1 TB/s.  Loads, start and merge alone take 82 to 88 % of
 // those two; with thousands of pairs the units' arithmetic is the larger part
 // (about 1460 SM cycles per e4m3 unit, bound by dependent latencies with eight
 // consumer warps per SM: 128 conversions, 64 MMAs and 32 byte regroupings per

@@ -44,8 +44,9 @@
 // Hot code is kept short and the rare paths (a masked block, a raised
 // reference) out of line: with twelve warps in five roles the instruction
 // cache decides.  With the rare paths inside loops unrolled over 128 columns
-// the same prompt took 1.37 ms.  Measured for it now: 0.76 ms, 1.08 PFLOP/s of
-// visible products (0.66 of cuBLAS's measured burst).  Per block (both tiles)
+// the same prompt took 1.37 ms.  Measured for it now: 0.76 ms in a single replay,
+// 1.08 PFLOP/s of visible products (0.66 of cuBLAS's measured burst); back to
+// back, at the card's power limit, 0.89 ms (0.57).  Per block (both tiles)
 // the S issuer spends about 2150 cycles issuing and the P V issuer 900, so the
 // tensor pipe is what the loop comes closest to; exponentials take about 1750
 // of a softmax warp's 3600.  Measured and not kept: every fourth exponential on
