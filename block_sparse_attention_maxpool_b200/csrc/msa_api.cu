@@ -1326,10 +1326,13 @@ int ext_attn(const msa_shape* sh, const msa_pages* pages, const msa_bf16* q, con
   }
   const bool by_streams = !expands_for_sure(sh, n_q);
   if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need) {
-      if (!by_streams) return MSA_ERR_WORKSPACE;
+    const bool room = workspace != nullptr && workspace_bytes >= need;
+    const bool aligned = (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0;
+    if (by_streams && !(room && aligned)) {
       need = 0;                                  // the cluster kernel does it too
-    } else if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) {
+    } else if (!room) {
+      return MSA_ERR_WORKSPACE;
+    } else if (!aligned) {
       return MSA_ERR_ALIGN;
     }
   }

@@ -309,9 +309,12 @@ def test_8bit_prompts_in_a_cache_of_many_slots(form):
         graph.replay()
         assert torch.equal(out, result)
     if form == "selection":
-        out.fill_(math.nan)
-        assert raw_sparse(shape, q, [kv[0][0], kv[1][0], kv[0][1], kv[1][1]], sel, stream, pos, 128 ** -0.5, out, pages=pages) == 0
-        assert torch.equal(out, one)
+        need = msa.msa_attn_workspace_bytes(shape, n, msa.MODE_PREFILL, True, pages)
+        large = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+        for ws, result in ((None, one), (large[:need - 1], one), (large[16:], one), (large[:need], want)):
+            out.fill_(math.nan)
+            assert raw_sparse(shape, q, [kv[0][0], kv[1][0], kv[0][1], kv[1][1]], sel, stream, pos, 128 ** -0.5, out, ws, pages) == 0
+            assert torch.equal(out, result)
     PW.device_error()
 
 
