@@ -323,7 +323,8 @@ def _held(t: torch.Tensor, stream) -> torch.Tensor:
     launches on, so that it is not reused before that stream is done with it."""
     if stream is not None and t.is_cuda:
         raw, dev = _stream(stream), t.get_device()
-        t.record_stream(torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev))
+        if raw != torch._C._cuda_getCurrentRawStream(dev):
+            t.record_stream(torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev))
     return t
 
 
