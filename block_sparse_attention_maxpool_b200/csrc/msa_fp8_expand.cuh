@@ -13,9 +13,9 @@
 // others), so where it matters the last CTA of the range kernel adds the blocks
 // up and chooses: the tiles, or the cluster kernel that reads the 8-bit cache
 // itself, where the blocks do not fit, the queries come from too many streams or
-// a selection over many blocks takes less time there.  The kernels of the side that was not chosen return at once
-// (9 to 14 us in all, 2112 queries).  Bound by bytes: 128 read and 256 written
-// per row.  (Converted inside the attention kernel by four warps of
+// a selection over many blocks takes less time there.  The kernels of the side
+// that was not chosen return at once (2048 queries: 9 to 26 us in all).  Bound by
+// bytes: 128 read and 256 written per row.  (Converted inside the attention kernel by four warps of
 // its own, block by block, the 2048-query selection on 16384 tokens took 1.04
 // ms instead of 0.66: the conversion of a block, about 4000 cycles next to the
 // softmax warps, paced the loop.)
@@ -59,7 +59,7 @@ struct Params {
   const uint8_t* v_cache;
   const float* k_scale;       // scale of cache row r: k_scale[r / 128]
   const float* v_scale;
-  uint4* k_out;               // bf16, rows as in k_cache
+  uint4* k_out;               // bf16, rows as in k_cache or in the pages of `table`
   uint4* v_out;
   int32_t* range;             // [S][2], zeroed: highest position + 1, capacity - lowest slot seen
   int32_t* ctl;               // [2]: CTAs of the range kernel that are done (zeroed), the choice (kTiles); null: neither
